@@ -29,6 +29,7 @@ EXPORTS = ("h3attn_plan_init", "h3attn_workspace_bytes", "h3attn_pool", "h3attn_
            "h3attn_dense_workspace_bytes", "h3attn_dense_biased", "h3attn_check", "h3attn_selftest_timeout", "h3attn_set_wait_polls",
            "h3attn_attend_host", "h3attn_merge", "h3attn_tail_workspace_bytes", "h3attn_tail_correct",
            "h3attn_qk8_workspace_bytes", "h3attn_quantize_qk", "h3attn_forward_qk8",
+           "h3attn_cache_workspace_bytes", "h3attn_cache_append", "h3attn_cache_read", "h3attn_cache_forward",
            "h3attn_strerror")
 
 
@@ -51,6 +52,22 @@ class Plan(ctypes.Structure):
 class Penalty(ctypes.Structure):
     _fields_ = [("strength", ctypes.c_float), ("window", ctypes.c_float), ("falloff", ctypes.c_float),
                 ("cap", ctypes.c_float)]
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("H", ctypes.c_int32), ("d", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("times", ctypes.c_void_p)]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("row_start", ctypes.c_void_p), ("length", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("n_pos", ctypes.c_int32), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 DEFAULT_PENALTY = (2.0, 0.20, 0.25, 6.0)
@@ -107,6 +124,17 @@ def lib():
         L.h3attn_forward_qk8.argtypes = [PP, _P, _P, _P, _P, _P, ctypes.POINTER(Penalty), _P, _P, _P, _P,
                                          ctypes.c_size_t, _P, ctypes.c_size_t, _P]
         L.h3attn_forward_qk8.restype = ctypes.c_int
+        CP, BP, I64 = ctypes.POINTER(_CacheStruct), ctypes.POINTER(_BatchStruct), ctypes.c_int64
+        L.h3attn_cache_workspace_bytes.argtypes = [CP, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+        L.h3attn_cache_workspace_bytes.restype = ctypes.c_size_t
+        L.h3attn_cache_append.argtypes = [CP, BP, _P, I64, I64, _P, I64, I64, ctypes.POINTER(_RopeStruct), _P, _P,
+                                          ctypes.c_size_t, _P]
+        L.h3attn_cache_append.restype = ctypes.c_int
+        L.h3attn_cache_read.argtypes = [CP, BP, _P, _P, _P, ctypes.c_size_t, _P]
+        L.h3attn_cache_read.restype = ctypes.c_int
+        L.h3attn_cache_forward.argtypes = [CP, BP, ctypes.c_int, ctypes.c_int, _P, I64, I64, ctypes.c_int,
+                                           ctypes.POINTER(Penalty), _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.h3attn_cache_forward.restype = ctypes.c_int
         L.h3attn_check.argtypes = [_P, _P]
         L.h3attn_check.restype = ctypes.c_int
         L.h3attn_set_wait_polls.argtypes = [ctypes.c_uint32]
@@ -343,6 +371,199 @@ def tail_correct(p: Plan, v, kv_sel, o, lse, ws, tail_ws=None, stream=None) -> N
     _raise(lib().h3attn_tail_correct(ctypes.byref(p), v.data_ptr(), kv_sel.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                      ws.data_ptr(), ws.numel(), tw.data_ptr(), tw.numel(), _stream(stream)),
            "tail_correct")
+
+
+# ------------------------------------------------------------- paged int8 cache
+
+
+def _want(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this type, shape (None: any extent) and device, or an error that says which."""
+    if not (t.dtype == dtype and t.device == device and t.is_contiguous() and t.dim() == len(shape)
+            and all(w is None or w == n for w, n in zip(shape, t.shape))):
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}, not "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    return t
+
+
+class Cache:
+    """Paged int8 cache (h3attn_cache): k, v int8 [n_pages, H, 64, d]; k_scale, v_scale float32 [n_pages, H]; times
+    float32 [n_pages, 64] or None.  ``empty`` allocates one; the tensors may also come from elsewhere."""
+
+    __slots__ = ("_t", "_c")
+
+    def __init__(self, k, v, k_scale, v_scale, times=None):
+        if not (k.is_cuda and k.dtype == torch.int8 and k.dim() == 4 and k.shape[2] == 64 and k.is_contiguous()):
+            raise ValueError("k must be contiguous CUDA int8 [n_pages, H, 64, d]")
+        n, H, _, d = k.shape
+        _want(v, "v", torch.int8, k.shape, k.device)
+        _want(k_scale, "k_scale", torch.float32, (n, H), k.device)
+        _want(v_scale, "v_scale", torch.float32, (n, H), k.device)
+        if times is not None:
+            _want(times, "times", torch.float32, (n, 64), k.device)
+        self._t = (k, v, k_scale, v_scale, times)
+        self._c = _CacheStruct(n, H, d, 64, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                               _dptr(times))
+
+    @classmethod
+    def empty(cls, n_pages: int, H: int, d: int, times: bool = False, device="cuda") -> "Cache":
+        k = torch.empty((n_pages, H, 64, d), dtype=torch.int8, device=device)
+        s = torch.empty((2, n_pages, H), dtype=torch.float32, device=device)
+        t = torch.full((n_pages, 64), float("nan"), device=device) if times else None
+        return cls(k, torch.empty_like(k), s[0], s[1], t)
+
+    k = property(lambda self: self._t[0])
+    v = property(lambda self: self._t[1])
+    k_scale = property(lambda self: self._t[2])
+    v_scale = property(lambda self: self._t[3])
+    times = property(lambda self: self._t[4])
+    n_pages = property(lambda self: self._c.n_pages)
+    H = property(lambda self: self._c.H)
+    d = property(lambda self: self._c.d)
+    device = property(lambda self: self._t[0].device)
+
+
+class Rope:
+    """Rotation table of appended keys (h3attn_rope): cos, sin float32 [n_pos, dim / 2]; index int32 [T], the table
+    row of each appended row, or None for its position in the sequence."""
+
+    __slots__ = ("_t", "_c")
+
+    def __init__(self, cos, sin, index=None, interleaved: bool = False):
+        _want(cos, "cos", torch.float32, (None, None), cos.device)
+        _want(sin, "sin", torch.float32, cos.shape, cos.device)
+        if index is not None:
+            _want(index, "index", torch.int32, (None,), cos.device)
+        self._t = (cos, sin, index)
+        self._c = _RopeStruct(cos.data_ptr(), sin.data_ptr(), _dptr(index), cos.shape[0], 2 * cos.shape[1],
+                              int(interleaved))
+
+
+def cache_workspace(c: Cache, H: int, T: int, B: int) -> torch.Tensor:
+    """Workspace of the cache calls for H query heads, T packed rows and B sequences."""
+    n = lib().h3attn_cache_workspace_bytes(ctypes.byref(c._c), H, T, B)
+    if n == 0:
+        raise H3Error(EINVAL, "cache_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=c.device)
+
+
+def _batch(c: Cache, T: int, row_start, length, page_table) -> _BatchStruct:
+    dev, i32 = c._t[0].device, torch.int32
+    _want(page_table, "page_table", i32, (None, None), dev)
+    B, width = page_table.shape
+    _want(row_start, "row_start", i32, (B + 1,), dev)
+    _want(length, "length", i32, (B,), dev)
+    return _BatchStruct(B, T, width, row_start.data_ptr(), length.data_ptr(), page_table.data_ptr())
+
+
+def _rows(t, name: str, H, d: int, device):
+    """A bf16 [H, T, d] tensor of any head and row stride (rows themselves contiguous)."""
+    if not (t.dtype == torch.bfloat16 and t.device == device and t.dim() == 3 and t.shape[2] == d
+            and (H is None or t.shape[0] == H) and (t.stride(2) == 1 or t.numel() == 0)):
+        raise ValueError(f"{name} must be bf16 [{'H' if H is None else H}, T, {d}] on {device} with contiguous rows")
+    return t
+
+
+def _strides(t):
+    """Head and row stride; that of an extent of one row or head does not matter and may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+class _on:
+    """The device and stream of a cache call: the cache's device is current inside, and so is the stream."""
+
+    __slots__ = ("stream", "_ctx")
+
+    def __init__(self, device, stream):
+        self._ctx = []
+        if device.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            self._ctx.append(torch.cuda.stream(stream))
+        self.stream = stream
+
+    def __enter__(self):
+        for x in self._ctx:
+            x.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *a):
+        for x in reversed(self._ctx):
+            x.__exit__(*a)
+
+
+def cache_append(c: Cache, k, v, row_start, length, page_table, rope: Optional[Rope] = None, row_times=None, ws=None,
+                 stream=None) -> None:
+    """Append rows to the cache (h3attn_cache_append): k, v bf16 [H, T, d] (any head and row strides that are multiples
+    of 8), packed row row_start[b] + i becomes row length[b] + i of sequence b; keys rotated by ``rope``."""
+    dev = c._t[0].device
+    H, T, d = c._c.H, k.shape[1] if k.dim() == 3 else -1, c._c.d
+    _rows(k, "k", H, d, dev)
+    if _rows(v, "v", H, d, dev).shape[1] != T:
+        raise ValueError("k and v must have the same rows")
+    b = _batch(c, T, row_start, length, page_table)
+    if rope is not None and (rope._t[0].device != dev or (rope._t[2] is not None and rope._t[2].shape[0] != T)):
+        raise ValueError("rope must be on the cache's device, its index of T entries")
+    if row_times is not None:
+        _want(row_times, "row_times", torch.float32, (T,), dev)
+    with _on(dev, stream) as st:
+        if ws is None:
+            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+        _raise(lib().h3attn_cache_append(c._c, b, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v),
+                                         rope._c if rope is not None else None, _dptr(row_times),
+                                         ws.data_ptr(), ws.numel(), st), "cache_append")
+
+
+def cache_read(c: Cache, row_start, first, page_table, T: Optional[int] = None, k_out=None, v_out=None, ws=None,
+               stream=None):
+    """Cached rows as bf16 [H, T, d] (h3attn_cache_read): packed row row_start[b] + i gets row first[b] + i of sequence
+    b.  T packed rows, or the buffers k_out and v_out (both, or one for K or V alone); returns (k, v)."""
+    dev = c._t[0].device
+    H, d = c._c.H, c._c.d
+    with _on(dev, stream) as st:
+        if k_out is None and v_out is None:
+            if T is None:
+                raise ValueError("cache_read needs T or an output buffer")
+            k_out = torch.empty((H, T, d), dtype=torch.bfloat16, device=dev)
+            v_out = torch.empty_like(k_out)
+        rows = T if T is not None else (k_out if k_out is not None else v_out).shape[1]
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is not None:
+                _want(t, name, torch.bfloat16, (H, rows, d), dev)
+        b = _batch(c, rows, row_start, first, page_table)
+        if ws is None:
+            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+        _raise(lib().h3attn_cache_read(c._c, b, _dptr(k_out), _dptr(v_out), ws.data_ptr(), ws.numel(), st),
+               "cache_read")
+    return k_out, v_out
+
+
+def cache_forward(c: Cache, q, row_start, length, page_table, causal: bool = False, pen=None, q_times=None,
+                  max_rows: Optional[int] = None, ws=None, out=None, lse: bool | torch.Tensor = False,
+                  stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of packed query rows q bf16 [H, T, d] over the cached rows [0, length[b]) of their sequence
+    (h3attn_cache_forward); (o, lse) is one partition for merge().  The penalty needs q_times (float32 [T], NaN for
+    rows without one) and the cache's times.  Rows of a new ``out`` that belong to no sequence are not written."""
+    dev = c._t[0].device
+    _rows(q, "q", None, c._c.d, dev)
+    H, T, d = q.shape
+    b = _batch(c, T, row_start, length, page_table)
+    pn = _pen(pen)
+    if q_times is not None:
+        _want(q_times, "q_times", torch.float32, (T,), dev)
+    if out is not None:
+        _want(out, "out", torch.bfloat16, (H, T, d), dev)
+    if isinstance(lse, torch.Tensor):
+        _want(lse, "lse", torch.float32, (H, T), dev)
+    with _on(dev, stream) as st:
+        o = torch.empty((H, T, d), dtype=torch.bfloat16, device=dev) if out is None else out
+        lse_t = lse if isinstance(lse, torch.Tensor) else (
+            torch.empty((H, T), dtype=torch.float32, device=dev) if lse else None)
+        if ws is None:
+            ws = cache_workspace(c, H, T, b.B)
+        _raise(lib().h3attn_cache_forward(c._c, b, H, max_rows or 0, q.data_ptr(), *_strides(q),
+                                          int(causal), pn, _dptr(q_times), o.data_ptr(), _dptr(lse_t), ws.data_ptr(),
+                                          ws.numel(), st), "cache_forward")
+    return o, lse_t
 
 
 def check(ws: torch.Tensor, stream=None) -> int:

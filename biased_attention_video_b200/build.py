@@ -9,8 +9,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libh3attn.so")
-SOURCES = ["api.cu", "attn.cu", "pool.cu", "route.cu", "route_static.cu", "merge.cu", "tail.cu", "pair.cu", "quant.cu"]
-HEADERS = ["ptx.cuh", "kernels.cuh", "fastmath.cuh", "softmax.cuh"]
+SOURCES = ["api.cu", "attn.cu", "pool.cu", "route.cu", "route_static.cu", "merge.cu", "tail.cu", "pair.cu", "quant.cu",
+           "api_cache.cu", "cache.cu", "cache_attn.cu"]
+HEADERS = ["ptx.cuh", "kernels.cuh", "fastmath.cuh", "softmax.cuh", "cache.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

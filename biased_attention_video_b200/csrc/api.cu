@@ -562,7 +562,7 @@ const char* h3attn_strerror(int status) {
     case H3ATTN_ECUDA: return "CUDA call or kernel launch failed";
     case H3ATTN_ETIMEOUT: return "a bounded device-side wait gave up";
     case H3ATTN_EWORKSPACE: return "workspace missing or too small";
-    case H3ATTN_EDATA: return "routed list holds a block index outside the video key blocks";
+    case H3ATTN_EDATA: return "device data out of range (routed block index; page id, row offset, length or rotation index of a cache call)";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,175 @@
+// Paged int8 cache of keys and values: what its kernels share.  See the cache
+// section of include/h3attn.h for the layout and the quantisation rule.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "kernels.cuh"
+
+namespace h3 {
+
+constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100, the smallest scale a block takes
+
+// h3attn_cache
+struct CacheRef {
+  int n_pages, H, d;
+  int8_t *k, *v;            // [n_pages][H][64][d]
+  float *k_scale, *v_scale; // [n_pages][H]
+  float* times;             // [n_pages][64] or null
+};
+
+// h3attn_batch: rows [row_start[b], row_start[b + 1]) of T packed rows belong to sequence b
+struct BatchRef {
+  int B, T, max_pages;
+  const int32_t* row_start;   // [B + 1]
+  const int32_t* length;      // [B]
+  const int32_t* page_table;  // [B][max_pages]
+};
+
+struct RopeRef {
+  const float *cos, *sin;  // [n_pos][dim / 2]; null: no rotation
+  const int32_t* index;    // [T] or null (the row's position)
+  int n_pos, dim, interleaved;
+};
+
+struct AppendParams {
+  CacheRef c;
+  BatchRef b;
+  RopeRef rope;
+  const uint16_t *k, *v;
+  long long k_head, k_row, v_head, v_row;  // strides in elements
+  const float* row_times;
+  int* status;
+};
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
+
+struct ReadParams {
+  CacheRef c;
+  BatchRef b;
+  uint16_t *k, *v;  // [H][T][d] or null
+  int* status;
+};
+cudaError_t launch_cache_read(const ReadParams& p, cudaStream_t stream);
+
+struct CacheAttnParams {
+  CacheRef c;
+  BatchRef b;
+  int H, group, causal;  // query heads, query heads of one K/V head
+  const uint16_t* q;
+  long long q_head, q_row;
+  const float* q_times;  // null: no penalty
+  uint16_t* o;           // [H][T][d]
+  float* lse;            // [H][T] or null
+  int* status;
+  float scale_log2;      // log2(e) / sqrt(d)
+  float window, inv_falloff, strength_log2, cap_log2;
+};
+cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t stream);
+
+// ------------------------------------------------------------ device side
+
+__device__ __forceinline__ void cache_report(int* status, int code) { atomicCAS(status, 0, code); }
+
+// Rows [first, first + n) of sequence b in the packed rows, forced into [0, T]
+// (offsets that are not ascending in [0, T] are reported).
+struct SeqRows {
+  int first, n;
+};
+__device__ __forceinline__ SeqRows seq_rows(const BatchRef& r, int b, int* status) {
+  const int a = __ldg(r.row_start + b), e = __ldg(r.row_start + b + 1);
+  const int first = min(max(a, 0), r.T), last = min(max(e, first), r.T);
+  if (first != a || last != e) cache_report(status, kStatusData);
+  return SeqRows{first, last - first};
+}
+
+// Cached rows of sequence b, forced into what its row of the page table holds.
+__device__ __forceinline__ int seq_length(const BatchRef& r, int b, int* status) {
+  const int n = __ldg(r.length + b);
+  const int held = min(max(n, 0), r.max_pages * kBlock);
+  if (held != n) cache_report(status, kStatusData);
+  return held;
+}
+
+// Piece x of the call: the rows of one sequence that lie in one page.  Pieces
+// are counted sequence by sequence; sequence b's rows take the positions from
+// length[b] on.  Called by every thread of a block of NT threads; b = -1 when
+// the call has no piece x.
+struct Piece {
+  int b, page_no, lo, hi;  // positions [lo, hi) of sequence b, inside its page page_no
+  int row;                 // packed row of position lo
+  int held;                // earlier rows of the page that stay
+};
+template <int NT>
+__device__ __forceinline__ Piece find_piece(const BatchRef& r, int x, int* status) {
+  __shared__ int warp_sum[NT / 32], found[5];  // found: sequence, its start, rows, first packed row, piece in it
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) found[0] = -1;
+  int base = 0;
+  for (int b0 = 0; b0 < r.B && base <= x; b0 += NT) {
+    const int b = b0 + tid;
+    int start = 0, n = 0, first = 0, cnt = 0;
+    if (b < r.B) {
+      const SeqRows s = seq_rows(r, b, status);
+      start = seq_length(r, b, status);
+      first = s.first;
+      n = min(s.n, r.max_pages * kBlock - start);
+      if (n < s.n) cache_report(status, kStatusData);
+      cnt = n > 0 ? (start + n - 1) / kBlock - start / kBlock + 1 : 0;
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int off = base;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) off += warp_sum[w];
+      base += warp_sum[w];
+    }
+    const int i = x - (off + incl - cnt);
+    if (i >= 0 && i < cnt) {
+      found[0] = b;
+      found[1] = start;
+      found[2] = n;
+      found[3] = first;
+      found[4] = i;
+    }
+  }
+  __syncthreads();
+  Piece p{};
+  p.b = found[0];
+  if (p.b >= 0) {
+    const int start = found[1], end = start + found[2];
+    p.page_no = start / kBlock + found[4];
+    p.lo = max(start, p.page_no * kBlock);
+    p.hi = min(end, (p.page_no + 1) * kBlock);
+    p.row = found[3] + p.lo - start;
+    p.held = p.lo - p.page_no * kBlock;
+  }
+  return p;
+}
+// an upper bound of the pieces, known without the device arrays: a sequence of
+// n rows lies in at most min(n, n / 64 + 2) pages
+inline unsigned max_pieces(const BatchRef& r) {
+  const long long a = r.T, b = (long long)r.T / kBlock + 2ll * r.B;
+  return (unsigned)(a < b ? a : b);
+}
+
+// Page id of a sequence's page page_no, or -1 (reported) if the table holds none of the cache's pages.
+__device__ __forceinline__ int page_id(const CacheRef& c, const BatchRef& r, int b, int page_no, int* status) {
+  const int id = __ldg(r.page_table + (size_t)b * r.max_pages + page_no);
+  if (id < 0 || id >= c.n_pages) {
+    cache_report(status, kStatusData);
+    return -1;
+  }
+  return id;
+}
+
+}  // namespace h3

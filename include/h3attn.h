@@ -72,7 +72,7 @@ extern "C" {
 #define H3ATTN_ECUDA (-4)        /* a CUDA runtime/driver call or launch failed */
 #define H3ATTN_ETIMEOUT (-5)     /* a bounded device-side wait gave up */
 #define H3ATTN_EWORKSPACE (-6)   /* workspace missing or too small */
-#define H3ATTN_EDATA (-7)        /* device found a corrupt routed list (index out of range) */
+#define H3ATTN_EDATA (-7)        /* device found an index out of range (routed list, page table, rows of a batch) */
 
 /* Segment ids of the packed sequence. */
 enum {
@@ -314,6 +314,118 @@ H3ATTN_API size_t h3attn_dense_workspace_bytes(int S);
 H3ATTN_API int h3attn_dense_biased(int H, int S, int d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                         const uint8_t* seg, const float* times, const h3attn_penalty* pen, uint16_t* o,
                         float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Paged int8 cache of keys and values, for rows that stay from one call to the
+ * next (a clip's text, references, audio and guide rows over the denoising
+ * steps; the frames already generated of a streaming run; the context of a
+ * token-by-token decode).  The pages have no counterpart.
+ *
+ * A page is one block of 64 consecutive rows of one sequence, all K/V heads:
+ *  k, v: int8 codes [n_pages][H][64][d]; k_scale, v_scale: float32
+ *  [n_pages][H]; value = code * scale of its page and head.  d 64 or 128,
+ *  block 64, k and v 16-byte aligned, scales 4-byte.
+ *  times: float32 [n_pages][64] (16-byte aligned) or NULL: the rows' guide times
+ *  in seconds for the temporal penalty, NaN for a row that is no guide row.
+ * Plain data; the caller owns the buffers.  No initial contents are needed: a
+ * page's first row sets its scale. */
+typedef struct {
+  int32_t n_pages, H, d, block;
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  float* times;
+} h3attn_cache;
+
+/* The sequences of one call over the cache.  Their rows are packed: sequence b
+ * has rows [row_start[b], row_start[b + 1]) of T (row_start int32 [B + 1],
+ * ascending in [0, T]; rows behind row_start[B] belong to no sequence and are
+ * neither read nor written).  length: int32 [B], cached rows (see each call).
+ * page_table: int32 [B][max_pages]: row j of sequence b is row j % 64 of page
+ * page_table[b][j / 64]; entries past the last row used are not read.
+ * Sequences may share pages that a call only reads; a page that a call appends
+ * to must belong to one sequence, once.  All three arrays are on the device,
+ * 4-byte aligned, and are read when the kernels run: a captured call takes the
+ * values of its replay.  Values outside their range are recorded in the status
+ * word (H3ATTN_EDATA): offsets and lengths are forced into range, a page id
+ * outside [0, n_pages) is skipped (its rows are dropped on append, read as 0,
+ * and not attended). */
+typedef struct {
+  int32_t B, T, max_pages;
+  const int32_t* row_start;
+  const int32_t* length;
+  const int32_t* page_table;
+} h3attn_batch;
+
+/* Rotation of the appended keys: pair (i, j) of columns becomes
+ * (x_i cos - x_j sin, x_j cos + x_i sin), with j = i + 1 for even i when
+ * interleaved, else j = i + dim / 2; dim (a multiple of 16, at most d) leading
+ * columns are rotated.  cos, sin: float32 [n_pos][dim / 2] on the device, 16-byte
+ * aligned, so a table may hold any mix of axes; index: int32 [T], the table row
+ * of each packed row, or NULL for its position in the sequence.  An index
+ * outside [0, n_pos) takes the nearest row and is recorded (H3ATTN_EDATA). */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  const int32_t* index;
+  int32_t n_pos, dim, interleaved;
+} h3attn_rope;
+
+/* Bytes of device workspace that the cache calls need for H query heads and a
+ * batch of B sequences with T packed rows: the status word, and for
+ * h3attn_cache_forward the partial results of sequences that several blocks
+ * share.  The caller allocates it once, zero-filled; h3attn_check reads and
+ * clears its status word.  Calls that overlap on the GPU must not share one.
+ * h3attn_cache_append and h3attn_cache_read need its first 256 bytes only. */
+H3ATTN_API size_t h3attn_cache_workspace_bytes(const h3attn_cache* cache, int H, int T, int B);
+
+/* Append rows: packed row row_start[b] + i becomes row length[b] + i of sequence
+ * b (length: the rows cached before this call).  k, v: bf16, head h and packed
+ * row t at h * head_stride + t * row_stride elements, d contiguous elements; the
+ * strides are multiples of 8 and the addresses 16-byte aligned.  rope NULL: the
+ * keys are stored as they are; the values are never rotated.
+ * Quantisation, in fp32 with every product, sum and quotient rounded to nearest:
+ *   a = max |y| over the call's rows of that page and head,
+ *   s' = max(the page's scale if it holds earlier rows of the sequence, a / 127, 2^-100),
+ *   code = clamp(rint(y * (1 / s')), -127, 127);
+ * earlier rows of a page whose scale grows are taken along:
+ * code' = rint(code * (s / s')).  A value that is not finite gives the page and
+ * head the scale NaN, and attention over the page is NaN.
+ * Rows of a page from position length[b] on are replaced and the ones behind
+ * the new rows are undefined: appending at a smaller length drops what was there.
+ * row_times: float32 [T] guide times (NaN: no guide row), or NULL for none;
+ * they need cache->times. */
+H3ATTN_API int h3attn_cache_append(const h3attn_cache* cache, const h3attn_batch* batch, const uint16_t* k,
+                                   int64_t k_head_stride, int64_t k_row_stride, const uint16_t* v,
+                                   int64_t v_head_stride, int64_t v_row_stride, const h3attn_rope* rope,
+                                   const float* row_times, void* ws, size_t ws_bytes, void* stream);
+
+/* Read rows back: packed row row_start[b] + i gets bf16(code * scale) of row
+ * length[b] + i of sequence b (length: the first row to read), so that cached
+ * keys and values can go through h3attn_route and h3attn_forward with others.
+ * k, v: bf16 [H][T][d], 16-byte aligned; either may be NULL. */
+H3ATTN_API int h3attn_cache_read(const h3attn_cache* cache, const h3attn_batch* batch, uint16_t* k, uint16_t* v,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of packed query rows over the cached rows [0, length[b]) of their
+ * sequence; with causal, row i of n sees rows j <= length[b] - n + i only (the n
+ * newest rows are the queries' own).  H query heads, a multiple of cache->H:
+ * query head h reads K/V head h / (H / cache->H).
+ *   score = q . k / sqrt(d) - penalty(|t_q - t_k|),
+ * the penalty (pen NULL: none) as in h3attn_forward for a query row and a cached
+ * row that both have a time (q_times float32 [T], NaN for a row that is no
+ * output row; cache->times).  A row that sees no key gets O = 0 and LSE = -inf,
+ * so that o and lse are one partition for h3attn_merge with any others.
+ * q: bf16 by strides, as k above; o: bf16 [H][T][d], 16-byte aligned; lse:
+ * float32 [H][T] natural-log normaliser or NULL.  Rows that belong to no
+ * sequence are left as they were.
+ * max_rows: no sequence has more rows in this call (0: not known); it chooses
+ * between kernels and does not change results beyond their rounding.
+ * ws: h3attn_cache_workspace_bytes(cache, H, T, B) bytes. */
+H3ATTN_API int h3attn_cache_forward(const h3attn_cache* cache, const h3attn_batch* batch, int H, int max_rows,
+                                    const uint16_t* q, int64_t q_head_stride, int64_t q_row_stride, int causal,
+                                    const h3attn_penalty* pen, const float* q_times, uint16_t* o, float* lse, void* ws,
+                                    size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return and clear the device-side status word
  * of ws: H3ATTN_OK, H3ATTN_ETIMEOUT or H3ATTN_EDATA; H3ATTN_ECUDA if the
