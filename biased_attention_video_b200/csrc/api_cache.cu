@@ -48,9 +48,10 @@ int check_ws(const void* ws, size_t have, size_t need) {
 
 bool finite_nonneg(float x) { return std::isfinite(x) && x >= 0.0f; }
 
+// status word | partial results
 size_t forward_bytes(int H, int Hkv, int d, int T, int B) {
-  (void)H, (void)Hkv, (void)d, (void)T, (void)B;
-  return kStatusBytes;
+  (void)B;
+  return kStatusBytes + h3::cache_rows_partial_bytes(d, (long long)T * (H / Hkv));
 }
 
 }  // namespace
@@ -144,7 +145,9 @@ int h3attn_cache_forward(const h3attn_cache* cache, const h3attn_batch* batch, i
   p.lse = lse;
   p.status = static_cast<int*>(ws);
   p.scale_log2 = 1.4426950408889634f / std::sqrt((float)p.c.d);
-  return h3::launch_cache_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ECUDA;
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  const long long rows = (long long)(max_rows > 0 && max_rows < p.b.T ? max_rows : p.b.T) * p.group;
+  return h3::launch_cache_rows(p, rows, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ECUDA;
 }
 
 }  // extern "C"

@@ -65,8 +65,13 @@ struct CacheAttnParams {
   int* status;
   float scale_log2;      // log2(e) / sqrt(d)
   float window, inv_falloff, strength_log2, cap_log2;
+  float* partial;        // partial results (see the kernels)
 };
-cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t stream);
+
+// Row tiles of 8 NT (query row, head of the group) pairs; see cache_rows.cu.
+size_t cache_rows_partial_bytes(int d, long long rows);
+// rows: most (query row, head of the group) pairs of one sequence
+cudaError_t launch_cache_rows(const CacheAttnParams& p, long long rows, cudaStream_t stream);
 
 // ------------------------------------------------------------ device side
 

@@ -513,3 +513,20 @@ def test_calls_on_another_stream_and_device_order():
         h3.cache_forward(c, q.float(), i32([0, 5]), i32([300]), i32(table))
     with pytest.raises(h3.H3Error):
         h3.cache_forward(c, torch.randn(3, 5, 128, device=DEV).to(torch.bfloat16), i32([0, 5]), i32([300]), i32(table))
+
+
+@pytest.mark.parametrize("rows", [6, 150])
+def test_a_marked_page_stays_away_from_rows_that_do_not_see_it(rows):
+    """Causal rows: the ones whose last key lies before the marked page are as they would be without it."""
+    c, host = make_cache(4, 1, 128, seed=12)
+    n = 128 + rows // 2                       # rows i < rows - n % 64 ... end before position 128
+    q = torch.randn(1, rows, 128, device=DEV).to(torch.bfloat16)
+    args = q, i32([0, rows]), i32([n]), i32([[0, 1, 2, 3]])
+    want, want_l = h3.cache_forward(c, *args, causal=True, lse=True)
+    for scale in (c.k_scale, c.v_scale):
+        scale[2, 0] = float("nan")
+    o, l = h3.cache_forward(c, *args, causal=True, lse=True)
+    clean = 128 - (n - rows)                  # row i sees keys up to n - rows + i
+    assert 0 < clean < rows
+    assert torch.equal(o[:, :clean], want[:, :clean]) and torch.equal(l[:, :clean], want_l[:, :clean])
+    assert torch.all(torch.isnan(o[:, clean:])) and torch.all(torch.isnan(l[:, clean:]))
