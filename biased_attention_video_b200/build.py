@@ -10,8 +10,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libh3attn.so")
 SOURCES = ["api.cu", "attn.cu", "pool.cu", "route.cu", "route_static.cu", "merge.cu", "tail.cu", "pair.cu", "quant.cu",
-           "api_cache.cu", "cache.cu", "cache_rows.cu"]
-HEADERS = ["ptx.cuh", "kernels.cuh", "fastmath.cuh", "softmax.cuh", "cache.cuh"]
+           "api_cache.cu", "cache.cu", "cache_rows.cu",
+           "cache_tiles.cu"]
+HEADERS = ["ptx.cuh", "kernels.cuh", "fastmath.cuh", "softmax.cuh", "cache.cuh",
+           "cache_attn.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

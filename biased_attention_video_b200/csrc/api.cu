@@ -172,9 +172,8 @@ int forward_impl(const h3attn_plan* plan, const uint16_t* q, const uint16_t* k, 
     p.strength_log2 = pen->strength * log2e;
     p.cap_log2 = pen->cap * log2e;
   }
-  const uint32_t polls = g_wait_polls.load(std::memory_order_relaxed);
-  p.wait_polls = polls == 0u ? kWaitPolls : polls;
-  p.wait_ns = kWaitNs;
+  p.wait_polls = h3::wait_poll_limit();
+  p.wait_ns = h3::wait_time_limit_ns();
   // routed: adjacent pairs over the dense prefix, then the overlap pairing
   p.qpairs = routed ? reinterpret_cast<const uint32_t*>(wsb + wl.pairs) : nullptr;
   p.n_dense_tiles = routed ? h3::paired_first_block(plan->first_video_block) / 2 : (plan->n_blocks + 1) / 2;
@@ -207,6 +206,12 @@ int forward_impl(const h3attn_plan* plan, const uint16_t* q, const uint16_t* k, 
 }  // namespace
 
 namespace h3 {
+uint32_t wait_poll_limit() {
+  const uint32_t polls = g_wait_polls.load(std::memory_order_relaxed);
+  return polls == 0u ? kWaitPolls : polls;
+}
+uint64_t wait_time_limit_ns() { return kWaitNs; }
+
 bool encode_u8_3d(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2, uint32_t box0,
                   uint32_t box1) {
   EncodeTiledFn fn = encode_fn();

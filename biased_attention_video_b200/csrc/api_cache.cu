@@ -48,10 +48,28 @@ int check_ws(const void* ws, size_t have, size_t need) {
 
 bool finite_nonneg(float x) { return std::isfinite(x) && x >= 0.0f; }
 
-// status word | partial results
-size_t forward_bytes(int H, int Hkv, int d, int T, int B) {
-  (void)B;
-  return kStatusBytes + h3::cache_rows_partial_bytes(d, (long long)T * (H / Hkv));
+// Up to this many (query row, head of the group) pairs of a sequence go through
+// the kernel for few rows.
+constexpr long long kFewPairs = 32;
+
+// status word | the tile kernel's line [B + 1] | partial results.  A batch whose
+// rows all fit the kernel for few rows needs no line.
+struct ForwardLayout {
+  size_t base, partial, total;
+};
+ForwardLayout forward_layout(int H, int Hkv, int d, int T, int B) {
+  const long long pairs = (long long)T * (H / Hkv);
+  ForwardLayout l;
+  l.base = kStatusBytes;
+  l.partial = l.base;
+  size_t partial = h3::cache_rows_partial_bytes(d, pairs);
+  if (pairs > kFewPairs) {
+    l.partial += ((size_t)(B + 1) * sizeof(long long) + 255) / 256 * 256;
+    const size_t tiles = h3::cache_tiles_partial_bytes(d);
+    if (tiles > partial) partial = tiles;
+  }
+  l.total = l.partial + partial;
+  return l;
 }
 
 }  // namespace
@@ -61,7 +79,7 @@ extern "C" {
 size_t h3attn_cache_workspace_bytes(const h3attn_cache* cache, int H, int T, int B) {
   if (cache == nullptr || cache->H < 1 || H < 1 || H % cache->H != 0 || T < 0 || B < 1) return 0;
   if (!(cache->d == 64 || cache->d == 128)) return 0;
-  return forward_bytes(H, cache->H, cache->d, T, B);
+  return forward_layout(H, cache->H, cache->d, T, B).total;
 }
 
 int h3attn_cache_append(const h3attn_cache* cache, const h3attn_batch* batch, const uint16_t* k, int64_t k_head_stride,
@@ -134,7 +152,8 @@ int h3attn_cache_forward(const h3attn_cache* cache, const h3attn_batch* batch, i
   if (int rc = check_strided(q, q_head_stride, q_row_stride)) return rc;
   if (o == nullptr) return H3ATTN_EINVAL;
   if (misaligned(o, 16) || misaligned(lse, 4)) return H3ATTN_EALIGN;
-  if (int rc = check_ws(ws, ws_bytes, forward_bytes(H, p.c.H, p.c.d, p.b.T, p.b.B))) return rc;
+  const ForwardLayout lay = forward_layout(H, p.c.H, p.c.d, p.b.T, p.b.B);
+  if (int rc = check_ws(ws, ws_bytes, lay.total)) return rc;
   p.H = H;
   p.group = H / p.c.H;
   p.causal = causal != 0;
@@ -145,9 +164,15 @@ int h3attn_cache_forward(const h3attn_cache* cache, const h3attn_batch* batch, i
   p.lse = lse;
   p.status = static_cast<int*>(ws);
   p.scale_log2 = 1.4426950408889634f / std::sqrt((float)p.c.d);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  const long long rows = (long long)(max_rows > 0 && max_rows < p.b.T ? max_rows : p.b.T) * p.group;
-  return h3::launch_cache_rows(p, rows, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ECUDA;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  p.base = reinterpret_cast<long long*>(wsb + lay.base);
+  p.partial = reinterpret_cast<float*>(wsb + lay.partial);
+  p.wait_polls = h3::wait_poll_limit();
+  p.wait_ns = h3::wait_time_limit_ns();
+  const long long pairs = (long long)(max_rows > 0 && max_rows < p.b.T ? max_rows : p.b.T) * p.group;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = pairs <= kFewPairs ? h3::launch_cache_rows(p, pairs, st) : h3::launch_cache_tiles(p, st);
+  return e == cudaSuccess ? H3ATTN_OK : H3ATTN_ECUDA;
 }
 
 }  // extern "C"

@@ -66,12 +66,19 @@ struct CacheAttnParams {
   float scale_log2;      // log2(e) / sqrt(d)
   float window, inv_falloff, strength_log2, cap_log2;
   float* partial;        // partial results (see the kernels)
+  long long* base;       // [B + 1], the tile kernel's line (see cache_tiles.cu)
+  uint32_t wait_polls;   // bounded waits of the tile kernel
+  uint64_t wait_ns;
 };
 
 // Row tiles of 8 NT (query row, head of the group) pairs; see cache_rows.cu.
 size_t cache_rows_partial_bytes(int d, long long rows);
 // rows: most (query row, head of the group) pairs of one sequence
 cudaError_t launch_cache_rows(const CacheAttnParams& p, long long rows, cudaStream_t stream);
+
+// Tensor-core tiles of 256 pairs; see cache_tiles.cu.
+size_t cache_tiles_partial_bytes(int d);
+cudaError_t launch_cache_tiles(const CacheAttnParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ device side
 

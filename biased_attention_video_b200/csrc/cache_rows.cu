@@ -22,13 +22,9 @@
 // The d order of A and of Q agree by construction and nothing else sees it, so
 // a lane takes 16 consecutive bytes of a row per load.  mma.sync and not tcgen05:
 // 8 rows fill no 128-row tile, and the widened codes are in registers anyway.
-// Widening: with bits 0x4300 in front, the low 7 bits of a code read as
-// 128 + low in bf16 and the sign bit alone as 128 or 256; their difference is
-// the code (two logic operations and one packed subtraction for two codes).
 #include <cuda_bf16.h>
 
-#include "cache.cuh"
-#include "softmax.cuh"
+#include "cache_attn.cuh"
 
 namespace h3 {
 namespace {
@@ -76,15 +72,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
-}
-
-// The codes in bytes 0 and 2 of w as two bf16.
-__device__ __forceinline__ uint32_t widen2(uint32_t w) {
-  uint32_t lo, hi, r;
-  asm("lop3.b32 %0, %1, 0x007F007F, 0x43004300, 0xEA;" : "=r"(lo) : "r"(w));  // (w & a) | b
-  asm("lop3.b32 %0, %1, 0x00800080, 0x43004300, 0xEA;" : "=r"(hi) : "r"(w));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(hi));
-  return r;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -176,17 +163,6 @@ __device__ __forceinline__ int find_seq(const CacheAttnParams& p, long long u, l
 __device__ __forceinline__ long long share_of(long long total) {
   const long long even = (total + kGrid - 1) / kGrid;
   return even > kMinShare ? even : kMinShare;
-}
-
-// Row r of a tile (pair r of the sequence's list): its packed row and head.
-__device__ __forceinline__ void store_row(const CacheAttnParams& p, const Seq& s, int hk, long long pair, int col,
-                                          float4 v, float m, float l) {
-  const int i = (int)(pair / p.group), h = hk * p.group + (int)(pair % p.group);
-  const size_t at = (size_t)h * p.b.T + s.first + i;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  *reinterpret_cast<uint2*>(p.o + at * p.c.d + col) =
-      make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-  if (p.lse != nullptr && col == 0) p.lse[at] = (m + log2f(l)) * kLn2;
 }
 
 // Slot of partial results: unnormalised O [R][D], then (maximum, sum) [R].
@@ -462,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
         sum.x += a * y.x, sum.y += a * y.y, sum.z += a * y.z, sum.w += a * y.w;
       }
       if (whole) {
-        store_row(p, s, hk, pair0 + r, col, sum, mm, ll);
+        store_cols(p, s.first, hk, pair0 + r, col, sum, mm, ll);
       } else {
         *reinterpret_cast<float4*>(slot + r * D + col) = sum;
         if (col == 0) *reinterpret_cast<float2*>(slot + R * D + 2 * r) = make_float2(mm, ll);
@@ -506,7 +482,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const CacheAttnParams p)
       sum.x = sum.x * a + e * y.x, sum.y = sum.y * a + e * y.y;
       sum.z = sum.z * a + e * y.z, sum.w = sum.w * a + e * y.w;
     }
-    store_row(p, s, hk, pair0 + r, col, sum, mm, ll);
+    store_cols(p, s.first, hk, pair0 + r, col, sum, mm, ll);
   }
 }
 

@@ -1,0 +1,720 @@
+// Attention over the paged int8 cache for many query rows per sequence, on the
+// tensor cores (tcgen05); the formulas are those of cache_rows.cu.
+//
+// The (query row, head of the group) pairs of a sequence and K/V head form one
+// list, row by row, cut into tiles of 256 pairs: two tcgen05 tiles A and B of
+// 128 rows that share every K and V block, so that a code is widened to bf16
+// once for 256 rows.  A step takes 128 keys (two pages): S = Q K^T runs at
+// N = 128, the tensor cores' full rate (N = 64 takes as long).  While the softmax
+// works on one tile's scores the tensor cores run the other's products.
+//
+// Warp roles (512 threads, one block per SM; the 128 registers a thread that the
+// block starts with are dealt out anew, 160 / 112 / 80 per warpgroup):
+//   warps 0..3, 4..7  softmax of tile A, B: one thread per pair (= TMEM lane);
+//                     they also bring Q in and the output out
+//   warps 8..11       keys and values: 16-byte loads of codes, held one step ahead
+//                     in registers, widened and stored as bf16 in the swizzled
+//                     layout the products read (two buffers of K and of V)
+//   warp 12           TMEM owner and single-thread tcgen05.mma issuer (13..15 idle)
+//
+// TMEM (512 columns): S_A [0, 128), S_B [128, 256), O_A from 256, O_B from 256 + d.
+// The bf16 probabilities go over the first 64 columns of their S.  Issue order:
+//   S_A(0) S_B(0) | PV_A(0) S_A(1) | PV_B(0) S_B(1) | PV_A(1) S_A(2) | ...
+// The products of one thread run in order: S_A(j+1) does not overwrite P_A(j)
+// before PV_A(j) has read it, and when S_A(j+1) is complete so is PV_A(j), so a
+// rescale of O_A needs no wait of its own.
+//
+// The columns of K, V and Q are stored with every group of four in the order
+// (0, 2, 1, 3), as the codes widen; the products do not see it, and O comes back
+// in the same order.
+//
+// Work split: an item is one tile of one sequence and K/V head, its units are the
+// steps up to the last key that any of its rows sees.  All items form one line,
+// sequence by sequence, head by head, tile by tile; the blocks share it evenly,
+// and an item that lies in several blocks is joined by another launch from
+// partial results (maximum, sum, unnormalised O in fp32).  The line is laid out
+// on the device (plan_kernel), for the lengths are read there.
+#include <cuda_bf16.h>
+
+#include "cache_attn.cuh"
+
+namespace h3 {
+namespace {
+
+using namespace sm;
+
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 12;
+constexpr int kWidenWarp = 8;
+constexpr int kTile = 256;   // pairs of an item
+constexpr int kStep = 128;   // keys of a step
+constexpr int kGrid = 148;   // one block per SM
+constexpr long long kMinShare = 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;
+
+// ---------------------------------------------------------------- the line
+
+struct Seq {
+  int first, n, len, tiles;
+};
+__device__ __forceinline__ Seq load_seq(const CacheAttnParams& p, int b) {
+  Seq s;
+  const SeqRows r = seq_rows(p.b, b, p.status);
+  s.first = r.first;
+  s.n = r.n;
+  s.len = seq_length(p.b, b, p.status);
+  s.tiles = (int)(((long long)s.n * p.group + kTile - 1) / kTile);
+  return s;
+}
+// Steps of tile t (one at least, so that rows that see nothing are written too).
+__device__ __forceinline__ int tile_steps(const CacheAttnParams& p, const Seq& s, int t) {
+  int seen = s.len;
+  if (p.causal) {
+    const long long pairs = (long long)s.n * p.group, last = min(pairs, (long long)(t + 1) * kTile) - 1;
+    seen = max(0, min(s.len, s.len - s.n + (int)(last / p.group) + 1));
+  }
+  return max(1, (seen + kStep - 1) / kStep);
+}
+
+// base[b]: the line before sequence b; base[B]: its length.  One block, one warp
+// per sequence at a time.
+__global__ void __launch_bounds__(1024) plan_kernel(const CacheAttnParams p) {
+  __shared__ long long units[32];
+  __shared__ long long before;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    before = 0;
+    p.base[0] = 0;
+  }
+  for (int b0 = 0; b0 < p.b.B; b0 += 32) {
+    const int b = b0 + warp;
+    long long u = 0;
+    if (b < p.b.B) {
+      const Seq s = load_seq(p, b);
+      if (p.causal) {
+        for (int t = lane; t < s.tiles; t += 32) u += tile_steps(p, s, t);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
+      } else {
+        u = (long long)s.tiles * tile_steps(p, s, 0);
+      }
+    }
+    if (lane == 0) units[warp] = u * p.c.H;
+    __syncthreads();
+    if (warp == 0) {
+      long long v = units[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long w = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += w;
+      }
+      const long long at = before + v;
+      if (b0 + lane < p.b.B) p.base[b0 + lane + 1] = at;
+      __syncwarp();
+      if (lane == 31) before = at;
+    }
+    __syncthreads();
+  }
+}
+
+// The item that unit u lies in, found by one warp; every lane gets it.
+struct Item {
+  int b, hk, first, n, len;
+  long long pair0;
+  int pairs;         // of the tile
+  int steps;         // of the whole item
+  long long start;   // the line before the item
+};
+__device__ __forceinline__ Item find_item(const CacheAttnParams& p, long long u) {
+  const int lane = threadIdx.x & 31;
+  Item it;
+  int b = 0;
+  for (int b0 = 0; b0 < p.b.B; b0 += 32) {
+    const unsigned in = __ballot_sync(kFull, b0 + lane < p.b.B && p.base[b0 + lane] <= u && u < p.base[b0 + lane + 1]);
+    if (in != 0u) {
+      b = b0 + __ffs(in) - 1;
+      break;
+    }
+  }
+  const Seq s = load_seq(p, b);
+  const long long lo = p.base[b], per_head = (p.base[b + 1] - lo) / p.c.H;
+  it.b = b;
+  it.first = s.first;
+  it.n = s.n;
+  it.len = s.len;
+  it.hk = (int)((u - lo) / per_head);
+  const long long head_lo = lo + it.hk * per_head;
+  int t = 0;
+  if (!p.causal) {
+    it.steps = tile_steps(p, s, 0);
+    t = (int)((u - head_lo) / it.steps);
+    it.start = head_lo + (long long)t * it.steps;
+  } else {
+    long long at = head_lo;
+    it.steps = 1;
+    it.start = head_lo;
+    for (int t0 = 0; t0 < s.tiles; t0 += 32) {
+      const int mine = t0 + lane < s.tiles ? tile_steps(p, s, t0 + lane) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(kFull, mine > 0 && u < at + incl);
+      if (past != 0u) {
+        const int l = __ffs(past) - 1;
+        t = t0 + l;
+        it.steps = __shfl_sync(kFull, mine, l);
+        it.start = at + __shfl_sync(kFull, incl, l) - it.steps;
+        break;
+      }
+      at += __shfl_sync(kFull, incl, 31);
+    }
+  }
+  it.pair0 = (long long)t * kTile;
+  it.pairs = (int)min((long long)kTile, (long long)s.n * p.group - it.pair0);
+  return it;
+}
+
+__device__ __forceinline__ long long share_of(long long total) {
+  const long long even = (total + kGrid - 1) / kGrid;
+  return even > kMinShare ? even : kMinShare;
+}
+
+// Slot of partial results: unnormalised O [256][D], then (maximum, sum) [256].
+// Block c's slot 0 holds an item that an earlier block began, slot 1 the item
+// that it begins and a later one goes on with.
+template <int D>
+__device__ __forceinline__ float* slot_of(const CacheAttnParams& p, long long block, int which) {
+  return p.partial + (2 * block + which) * (size_t)(kTile * (D + 2));
+}
+
+// --------------------------------------------------------------- the kernel
+
+// What the softmax needs to know of a page.
+struct PageMeta {
+  float c;      // K scale, log2 units: score = c * (q . code)
+  float lv;     // log2 of the V scale
+  float iv, vs; // 1 / V scale, V scale
+  int live;     // valid keys: 0 for a page past the end or outside the cache
+  int mode;     // guide times of its keys: 0 none, 1 all the same (t), 2 several
+  float t;
+  int plain;    // 64 valid keys, V scale in the range in which it goes into the exponent
+};
+constexpr float kPlainScale = 8.673617379884035e-19f;  // 2^-60: p vs >= 2^-126 for p >= 2^-66
+
+template <int D>
+struct TilesLayout {
+  static constexpr int kHalves = D / 64;       // 128-byte swizzle atoms along d
+  static constexpr int kAtom = 128 * 128;      // one 128-byte-wide column of 128 rows
+  static constexpr int kBlockBytes = kHalves * kAtom;  // a Q tile, a K or V block
+  static constexpr int kQ = 0;                 // tiles A, B
+  static constexpr int kK = 2 * kBlockBytes;   // two buffers
+  static constexpr int kV = 4 * kBlockBytes;   // two buffers
+  static constexpr int kMetaSlots = 4;
+  static constexpr int kMeta = 6 * kBlockBytes;                // [4] x 2 pages
+  static constexpr int kTimes = kMeta + kMetaSlots * 2 * (int)sizeof(PageMeta);  // [4][128]
+  static constexpr int kBars = kTimes + kMetaSlots * kStep * 4;
+  static constexpr int kNumBars = 2 + 2 + 2 + 2 + 4 + 1 + 2 + 2 + 1 + 1;
+  static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM base, abort flag
+  static constexpr int kItem = kMisc + 16;
+  static constexpr int kBytes = 1024 + kItem + (int)sizeof(Item) + 16;
+};
+
+// The whole block, from roles that run different code.
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+template <int D, bool kPen>
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParams p) {
+  using L = TilesLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t *k_full = bar, *k_empty = bar + 2, *v_full = bar + 4, *v_empty = bar + 6, *m_full = bar + 8,
+           *q_full = bar + 12, *s_full = bar + 13, *p_full = bar + 15, *o_final = bar + 17, *drain = bar + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  Item* item_slot = reinterpret_cast<Item*>(smem + L::kItem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const long long total = p.base[p.b.B], share = share_of(total);
+  const long long u0 = blockIdx.x * share, u1 = min(total, u0 + share);
+  if (u0 >= u1) return;
+  // an earlier call or block that gave up leaves the status word set
+  if (tid == 0) *abort_flag = *reinterpret_cast<volatile int*>(p.status) == kStatusTimeout ? 1 : 0;
+  __syncthreads();
+  if (*abort_flag) return;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 4);
+      mbar_init(v_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+    }
+    for (int i = 0; i < L::kMetaSlots; ++i) mbar_init(m_full + i, 4);
+    mbar_init(q_full, 8);
+    mbar_init(o_final, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Every role walks the block's items in step.  next(): the next item, the same
+  // for all (found by the first warp of the idle ones), or false at the end or
+  // after a give-up.
+  long long u = u0;
+  Item it;
+  int step0 = 0, n = 0, subs = 0;
+  uint32_t items = 0;               // items before
+  uint32_t done = 0, done_b = 0;    // their steps, and the steps of those with a tile B
+  auto next = [&]() -> bool {
+    if (n > 0) {
+      ++items;
+      done += (uint32_t)n;
+      if (subs == 2) done_b += (uint32_t)n;
+      u += n;
+    }
+    // every role is done with the last item's buffers
+    __syncwarp();
+    tc_fence_before();
+    block_sync();
+    tc_fence_after();
+    if (u >= u1 || *abort_flag) return false;
+    if (warp == kMmaWarp + 1) {
+      const Item x = find_item(p, u);
+      if (lane == 0) *item_slot = x;
+      __syncwarp();
+    }
+    block_sync();
+    it = *item_slot;
+    step0 = (int)(u - it.start);
+    n = (int)min((long long)it.steps, u1 - it.start) - step0;
+    subs = it.pairs > 128 ? 2 : 1;
+    return true;
+  };
+
+  // 2 x 128 x 160 + 128 x 112 + 128 x 80 = 512 x 128 registers
+  if (warp < kWidenWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    while (next()) {
+      // --------------------------------------------- Q, softmax, output
+      const int sub = warp >> 2, r = tid & 127;  // r: row of the tile = TMEM lane
+      const int pr = sub * 128 + r;
+      const bool valid = pr < it.pairs;
+      const long long pair = it.pair0 + pr;
+      const int row = valid ? (int)(pair / p.group) : 0;
+      {
+        const uint16_t* src = p.q + (it.hk * p.group + (valid ? (int)(pair % p.group) : 0)) * p.q_head +
+                              (long long)(it.first + row) * p.q_row;
+        uint8_t* dst = smem + L::kQ + sub * L::kBlockBytes + r * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (valid) w = __ldg(reinterpret_cast<const uint4*>(src) + c);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * L::kAtom + (((c & 7) ^ (r & 7)) << 4)) =
+              make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632),
+                         __byte_perm(w.z, w.w, 0x5410), __byte_perm(w.z, w.w, 0x7632));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      if (sub < subs) {
+        const int lim = valid && p.causal ? max(0, min(it.len, it.len - it.n + row + 1)) : it.len;
+        const int lim_all = __reduce_min_sync(kFull, lim);
+        const float tq = kPen && valid ? __ldg(p.q_times + it.first + row) : NAN;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_addr + (uint32_t)(128 * sub);
+        const uint32_t t_o = tmem + lane_addr + kTmemO + (uint32_t)(D * sub);
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+
+        // the step's running maximum becomes at least mx; O and l follow
+        auto raise = [&](float mx) {
+          const bool grow = mx > m + kRescaleThreshold;
+          const bool rescale = grow && m > -INFINITY;
+          const float alpha = rescale ? ex2(m - mx) : 1.0f;
+          if (grow) m = mx;
+          if (__any_sync(kFull, rescale)) {
+            l *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float x[32];
+              uint32_t y[32];
+              __syncwarp();
+              tmem_ld32f(t_o + c * 32, x);
+              tmem_landed(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[i] * alpha);
+              tmem_st32(t_o + c * 32, y);
+            }
+          }
+        };
+        auto top64 = [&](const float (&x)[32], const float (&y)[32]) -> float {
+          float mp[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mp[i] = fmaxf(x[i], y[i]);
+#pragma unroll
+          for (int i = 4; i < 32; ++i) mp[i & 3] = max3f(mp[i & 3], x[i], y[i]);
+          return fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]);
+        };
+
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t q = done + j;
+          const int slot = q & 3;
+          ok = __all_sync(kFull, wait_bar(m_full + slot, (q >> 2) & 1u, p, abort_flag));
+          if (!ok) break;
+          const PageMeta* meta = reinterpret_cast<const PageMeta*>(smem + L::kMeta) + 2 * slot;
+          const PageMeta pa = meta[0], pb = meta[1];
+          const float* times = reinterpret_cast<const float*>(smem + L::kTimes) + slot * kStep;
+          const int key0 = (step0 + j) * kStep;
+          const bool plain = pa.plain && pb.plain && key0 + kStep <= lim_all;
+          const float pen_a = kPen && pa.mode == 1 ? block_penalty_log2(tq, pa.t, p) : 0.0f;
+          const float pen_b = kPen && pb.mode == 1 ? block_penalty_log2(tq, pb.t, p) : 0.0f;
+          ok = __all_sync(kFull, wait_bar(s_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (plain) {
+            float x[32], y[32];
+            uint32_t pk[32];
+            auto fetch = [&](int col) {
+              __syncwarp();
+              tmem_ld32f(t_s + col, x);
+              tmem_ld32f(t_s + col + 32, y);
+              tmem_landed(x);
+              tmem_landed(y);
+            };
+            fetch(64);
+            float mx = top64(x, y) * pb.c - pen_b;
+            fetch(0);
+            mx = fmaxf(mx, top64(x, y) * pa.c - pen_a);
+            raise(mx);
+            auto probs = [&](const PageMeta& pg, float pen) {
+              const float off = pg.lv - m - pen;
+              float s0 = probs16_fast(x, off, pg.c, pk), s1 = probs16_fast(x + 16, off, pg.c, pk + 8);
+              s0 += probs16_fast(y, off, pg.c, pk + 16);
+              s1 += probs16_fast(y + 16, off, pg.c, pk + 24);
+              l = fmaf(s0 + s1, pg.iv, l);
+            };
+            probs(pa, pen_a);
+            __syncwarp();
+            tmem_st32(t_s, pk);
+            fetch(64);
+            probs(pb, pen_b);
+            __syncwarp();
+            tmem_st32(t_s + 32, pk);
+          } else {
+            // validity, visibility and penalty key by key
+            auto score = [&](float raw, int key, const PageMeta& pg, float pen) -> float {
+              if ((key & 63) >= pg.live || key0 + key >= lim) return -INFINITY;
+              if (kPen && pg.mode == 2) pen = block_penalty_log2(tq, times[key], p);
+              return raw * pg.c - pen;
+            };
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float x[32];
+              __syncwarp();
+              tmem_ld32f(t_s + c * 32, x);
+              tmem_landed(x);
+              const PageMeta& pg = c < 2 ? pa : pb;
+              const float pen = c < 2 ? pen_a : pen_b;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, score(x[i], c * 32 + i, pg, pen));
+            }
+            raise(mx);
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[32];
+              const PageMeta& pg = c == 0 ? pa : pb;
+              const float pen = c == 0 ? pen_a : pen_b;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                float x[32];
+                __syncwarp();
+                tmem_ld32f(t_s + c * 64 + half * 32, x);
+                tmem_landed(x);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const int key = c * 64 + half * 32 + i;
+                  const float e0 = ex2(score(x[i], key, pg, pen) - base);
+                  const float e1 = ex2(score(x[i + 1], key + 1, pg, pen) - base);
+                  l += e0 + e1;
+                  // a scale that is not finite stays away from rows that do not see the key
+                  pk[half * 16 + i / 2] = pack_bf16(e0 == 0.0f ? 0.0f : e0 * pg.vs, e1 == 0.0f ? 0.0f : e1 * pg.vs);
+                }
+              }
+              __syncwarp();
+              tmem_st32(t_s + c * 32, pk);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + sub);
+        }
+        // ------------------------------------------------------- output
+        if (ok) ok = __all_sync(kFull, wait_bar(o_final, items & 1u, p, abort_flag));
+        if (ok) {
+          tc_fence_after();
+          const bool whole = n == it.steps;
+          float* slot = whole ? nullptr : slot_of<D>(p, blockIdx.x, step0 > 0 ? 0 : 1);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float x[32];
+            __syncwarp();
+            tmem_ld32f(t_o + c * 32, x);
+            tmem_landed(x);
+            if (valid) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 v = make_float4(x[i], x[i + 2], x[i + 1], x[i + 3]);
+                if (whole) store_cols(p, it.first, it.hk, pair, c * 32 + i, v, m, l);
+                else *reinterpret_cast<float4*>(slot + pr * D + c * 32 + i) = v;
+              }
+            }
+          }
+          if (!whole && valid) *reinterpret_cast<float2*>(slot + kTile * D + 2 * pr) = make_float2(m, l);
+        }
+        // a step left early may still have TMEM accesses in flight
+        tmem_wait_st();
+        tmem_wait_ld();
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    while (next()) {
+      // ------------------------------------------------- keys and values
+      constexpr int kLoads = D / 16;  // 16-byte loads of a thread per K or V block
+      const int w = warp - kWidenWarp, page_of = w >> 1;
+      const int rlo = lane >> 2, ch = lane & 3;
+      // load i: row 32 w + 8 (i / halves) + rlo, 16 codes at 64 (i % halves) + 16 ch
+      uint4 kr[kLoads], vr[kLoads];
+      int page = -1;
+      auto find_page = [&](int j) {  // this warp's page of step j, -1 if it holds no valid key
+        const int no = (step0 + j) * 2 + page_of;
+        page = j < n && no * kBlock < it.len ? page_id(p.c, p.b, it.b, no, p.status) : -1;
+      };
+      auto load = [&](const int8_t* codes, uint4 (&x)[kLoads]) {
+        const int8_t* src = codes + ((size_t)max(page, 0) * p.c.H + it.hk) * kBlock * D;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int row = (w & 1) * 32 + i / L::kHalves * 8 + rlo;
+          x[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                          : __ldg(reinterpret_cast<const uint4*>(src + row * D + i % L::kHalves * 64 + ch * 16));
+        }
+      };
+      auto widen = [&](uint8_t* block, const uint4 (&x)[kLoads]) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int row = w * 32 + i / L::kHalves * 8 + rlo;
+          uint8_t* dst = block + i % L::kHalves * L::kAtom + row * 128;
+          *reinterpret_cast<uint4*>(dst + (((2 * ch) ^ (row & 7)) << 4)) =
+              make_uint4(widen2(x[i].x), widen2(x[i].x >> 8), widen2(x[i].y), widen2(x[i].y >> 8));
+          *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (row & 7)) << 4)) =
+              make_uint4(widen2(x[i].z), widen2(x[i].z >> 8), widen2(x[i].w), widen2(x[i].w >> 8));
+        }
+      };
+      // the page's scales and times, one step ahead like its codes
+      float ks = 0.0f, vs = 1.0f, t0 = NAN, t1 = NAN;
+      auto load_meta = [&]() {
+        ks = vs = 1.0f;
+        t0 = t1 = NAN;
+        if (page >= 0) {
+          ks = __ldg(p.c.k_scale + (size_t)page * p.c.H + it.hk);
+          vs = __ldg(p.c.v_scale + (size_t)page * p.c.H + it.hk);
+          if (kPen) {
+            t0 = __ldg(p.c.times + (size_t)page * kBlock + lane);
+            t1 = __ldg(p.c.times + (size_t)page * kBlock + 32 + lane);
+          }
+        }
+      };
+      find_page(0);
+      load(p.c.k, kr);
+      load(p.c.v, vr);
+      load_meta();
+      for (int j = 0; j < n; ++j) {
+        const uint32_t q = done + j;
+        const int s = q & 1, slot = q & 3;
+        const uint32_t ph = (q >> 1) & 1u;
+        if (!__all_sync(kFull, wait_bar(k_empty + s, ph ^ 1u, p, abort_flag))) break;
+        // keys of the page that rows may see: 0 for a page past the end or outside the cache
+        const int live = page < 0 ? 0 : max(0, min(kBlock, it.len - ((step0 + j) * 2 + page_of) * kBlock));
+        if ((w & 1) == 0) {
+          PageMeta pm;
+          pm.c = ks * p.scale_log2;
+          pm.vs = vs;
+          pm.lv = log2f(vs);
+          pm.iv = 1.0f / vs;
+          pm.live = live;
+          pm.mode = 0;
+          pm.t = 0.0f;
+          if (kPen) {
+            // a key past the end counts as one without a time
+            if (lane >= live) t0 = NAN;
+            if (lane + 32 >= live) t1 = NAN;
+            pm.t = __shfl_sync(kFull, t0, 0);
+            if (__all_sync(kFull, t0 == pm.t && t1 == pm.t)) pm.mode = 1;
+            else if (__any_sync(kFull, t0 == t0 || t1 == t1)) pm.mode = 2;
+            float* times = reinterpret_cast<float*>(smem + L::kTimes) + slot * kStep + page_of * kBlock;
+            times[lane] = t0;
+            times[lane + 32] = t1;
+          }
+          pm.plain = live == kBlock && pm.mode != 2 && vs >= kPlainScale && vs < 1e30f;
+          if (lane == 0) reinterpret_cast<PageMeta*>(smem + L::kMeta)[2 * slot + page_of] = pm;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m_full + slot);
+        widen(smem + L::kK + s * L::kBlockBytes, kr);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + s);
+        find_page(j + 1);
+        load(p.c.k, kr);
+        load_meta();
+        if (!__all_sync(kFull, wait_bar(v_empty + s, ph ^ 1u, p, abort_flag))) break;
+        widen(smem + L::kV + s * L::kBlockBytes, vr);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + s);
+        load(p.c.v, vr);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    while (next()) {
+      if (warp != kMmaWarp || lane != 0) continue;
+      // ------------------------------------------------------ MMA issuer
+      constexpr uint32_t kIdescS = idesc_bf16_f32(128, kStep, 0, 0);
+      constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, 0, 1);
+      // a descriptor's low bits hold the address / 16
+      const uint64_t q_d = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
+      const uint64_t k_d = sw128_desc(smem_u32(smem + L::kK), 16, 1024);
+      const uint64_t v_d = sw128_desc(smem_u32(smem + L::kV), L::kAtom, 1024);
+      auto issue_s = [&](int sub, uint32_t buf) {
+#pragma unroll
+        for (int kk = 0; kk < L::kHalves * 4; ++kk) {
+          const uint32_t off = (kk >> 2) * L::kAtom + (kk & 3) * 32;
+          umma_ss(tmem + (uint32_t)(128 * sub), q_d + ((sub * L::kBlockBytes + off) >> 4),
+                  k_d + ((buf * L::kBlockBytes + off) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full + sub);
+      };
+      bool ok = wait_bar(q_full, items & 1u, p, abort_flag) &&
+                wait_bar(k_full + (done & 1u), (done >> 1) & 1u, p, abort_flag);
+      if (ok) {
+        tc_fence_after();
+        for (int sub = 0; sub < subs; ++sub) issue_s(sub, done & 1u);
+        umma_commit(k_empty + (done & 1u));
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const uint32_t q = done + j, buf = q & 1u, ph = (q >> 1) & 1u, next = (q + 1) & 1u;
+        for (int sub = 0; ok && sub < subs; ++sub) {
+          ok = wait_bar(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
+          if (ok && sub == 0) ok = wait_bar(v_full + buf, ph, p, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            umma_ts(tmem + kTmemO + (uint32_t)(D * sub), tmem + (uint32_t)(128 * sub + 8 * kk),
+                    v_d + ((buf * L::kBlockBytes + kk * 2048) >> 4), kIdescO, j > 0 || kk > 0 ? 1u : 0u);
+          if (sub == subs - 1) umma_commit(v_empty + buf);
+          if (j + 1 < n) {
+            if (sub == 0) ok = wait_bar(k_full + next, ((q + 1) >> 1) & 1u, p, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(sub, next);
+            if (sub == subs - 1) umma_commit(k_empty + next);
+          }
+        }
+      }
+      umma_commit(o_final);
+    }
+  }
+
+  if (tid == kMmaWarp * 32) {  // all issued MMAs complete before TMEM is released
+    umma_commit(drain);
+    drain_wait(drain, 0, p);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the items that several blocks share: blocks (x, y) look at the border
+// between the stretches x and x + 1 and join the item that lies across it, if it
+// is that item's first border; y takes 32 of its pairs.
+template <int D>
+__global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p) {
+  __shared__ Item item;
+  const long long total = p.base[p.b.B], share = share_of(total);
+  const long long c0 = blockIdx.x, u = (c0 + 1) * share;
+  if (u >= total) return;
+  if (threadIdx.x < 32) {
+    const Item it = find_item(p, u);
+    if (threadIdx.x == 0) item = it;
+  }
+  __syncthreads();
+  const Item it = item;
+  if (it.start == u || it.start / share != c0) return;
+  const long long c1 = (it.start + it.steps - 1) / share;
+  const int r0 = blockIdx.y * 32;
+  for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
+    const int r = r0 + i / (D / 4), col = i % (D / 4) * 4;
+    if (r >= it.pairs) break;
+    float mm = -INFINITY, ll = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (long long c = c0; c <= c1; ++c) {
+      const float* slot = slot_of<D>(p, c, c == c0 ? 1 : 0);
+      const float2 x = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * r);
+      const float4 y = *reinterpret_cast<const float4*>(slot + r * D + col);
+      const float mn = fmaxf(mm, x.x), base = mn == -INFINITY ? 0.0f : mn;
+      const float a = ex2(mm - base), e = ex2(x.x - base);
+      mm = mn;
+      ll = ll * a + e * x.y;
+      sum.x = sum.x * a + e * y.x, sum.y = sum.y * a + e * y.y;
+      sum.z = sum.z * a + e * y.z, sum.w = sum.w * a + e * y.w;
+    }
+    store_cols(p, it.first, it.hk, it.pair0 + r, col, sum, mm, ll);
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
+  constexpr int bytes = TilesLayout<D>::kBytes;
+  auto kernel = p.q_times != nullptr ? tiles_kernel<D, true> : tiles_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  plan_kernel<<<1, 1024, 0, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  kernel<<<kGrid, kThreads, bytes, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  join_tiles_kernel<D><<<dim3(kGrid - 1, kTile / 32), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_tiles_partial_bytes(int d) { return (size_t)2 * kGrid * kTile * (d + 2) * sizeof(float); }
+
+cudaError_t launch_cache_tiles(const CacheAttnParams& p, cudaStream_t stream) {
+  return p.c.d == 64 ? launch_t<64>(p, stream) : launch_t<128>(p, stream);
+}
+
+}  // namespace h3

@@ -145,6 +145,10 @@ struct MergeParts {
 cudaError_t launch_merge(const MergeParts& parts, long long rows, int d, uint16_t* o, float* lse,
                          cudaStream_t stream);
 
+// Bounds of every device-side wait of the calls launched next (h3attn_set_wait_polls).
+uint32_t wait_poll_limit();
+uint64_t wait_time_limit_ns();
+
 cudaError_t launch_selftest_timeout(int* status, uint32_t polls, cudaStream_t stream);
 
 }  // namespace h3

@@ -29,8 +29,8 @@ __device__ __forceinline__ void report(int* status, int code) { atomicCAS(status
 
 // Bounded wait with CTA-wide abort.  On give-up: raise the CTA abort flag and
 // the global status word.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const AttnParams& p,
-                                         volatile int* abort) {
+template <class Params>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Params& p, volatile int* abort) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -52,7 +52,8 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const A
 
 // Wait used only while draining in-flight async work before exit: ignores
 // the abort flag, still bounded.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const AttnParams& p) {
+template <class Params>
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const Params& p) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return;
@@ -68,7 +69,8 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const
   }
 }
 
-__device__ __forceinline__ float block_penalty_log2(float tq, float tk, const AttnParams& p) {
+template <class Params>
+__device__ __forceinline__ float block_penalty_log2(float tq, float tk, const Params& p) {
   const float dt = fabsf(tq - tk);
   const float ex = fmaxf(dt - p.window, 0.0f) * p.inv_falloff;
   return fminf(p.strength_log2 * ex * ex, p.cap_log2);
