@@ -43,18 +43,35 @@ __device__ __forceinline__ void tmem_landed(float (&r)[32]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 
-// Columns [col, col + 4) of a pair's row of the output, and its LSE: the pair
-// (query row, head of the group) is number `pair` in the list of the sequence
-// whose packed rows begin at `first`; v unnormalised, m in log2 units.
-__device__ __forceinline__ void store_cols(const CacheAttnParams& p, int first, int hk, long long pair, int col,
-                                           float4 v, float m, float l) {
-  const int i = (int)(pair / p.group), h = hk * p.group + (int)(pair % p.group);
-  const size_t at = (size_t)h * p.b.T + first + i;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+// 16 columns of the warp's TMEM lanes
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Columns [col, col + 4) of output row `at` (head T + packed row) from unnormalised v; inv = 1 / sum, 0 for no key.
+__device__ __forceinline__ void store_cols(const CacheAttnParams& p, size_t at, int col, float4 v, float inv) {
   *reinterpret_cast<uint2*>(p.o + at * p.c.d + col) =
       make_uint2(sm::pack_bf16(v.x * inv, v.y * inv), sm::pack_bf16(v.z * inv, v.w * inv));
-  if (p.lse != nullptr && col == 0) p.lse[at] = (m + log2f(l)) * sm::kLn2;
+}
+// Its LSE from the maximum (log2 units) and the sum.
+__device__ __forceinline__ void store_lse(const CacheAttnParams& p, size_t at, float m, float l) {
+  if (p.lse != nullptr) p.lse[at] = (m + log2f(l)) * sm::kLn2;
 }
 
 }  // namespace h3

@@ -165,6 +165,11 @@ __device__ __forceinline__ long long share_of(long long total) {
   return even > kMinShare ? even : kMinShare;
 }
 
+// Output row (head T + packed row) of a pair of the sequence's list.
+__device__ __forceinline__ size_t row_of(const CacheAttnParams& p, const Seq& s, int hk, long long pair) {
+  return (size_t)(hk * p.group + (int)(pair % p.group)) * p.b.T + s.first + (int)(pair / p.group);
+}
+
 // Slot of partial results: unnormalised O [R][D], then (maximum, sum) [R].
 // Block c's slot 0 holds an item that an earlier block began, slot 1 the item
 // that it begins and a later one goes on with.
@@ -438,7 +443,9 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
         sum.x += a * y.x, sum.y += a * y.y, sum.z += a * y.z, sum.w += a * y.w;
       }
       if (whole) {
-        store_cols(p, s.first, hk, pair0 + r, col, sum, mm, ll);
+        const size_t at = row_of(p, s, hk, pair0 + r);
+        store_cols(p, at, col, sum, ll == 0.0f ? 0.0f : 1.0f / ll);
+        if (col == 0) store_lse(p, at, mm, ll);
       } else {
         *reinterpret_cast<float4*>(slot + r * D + col) = sum;
         if (col == 0) *reinterpret_cast<float2*>(slot + R * D + 2 * r) = make_float2(mm, ll);
@@ -482,7 +489,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const CacheAttnParams p)
       sum.x = sum.x * a + e * y.x, sum.y = sum.y * a + e * y.y;
       sum.z = sum.z * a + e * y.z, sum.w = sum.w * a + e * y.w;
     }
-    store_cols(p, s.first, hk, pair0 + r, col, sum, mm, ll);
+    const size_t at = row_of(p, s, hk, pair0 + r);
+    store_cols(p, at, col, sum, ll == 0.0f ? 0.0f : 1.0f / ll);
+    if (col == 0) store_lse(p, at, mm, ll);
   }
 }
 

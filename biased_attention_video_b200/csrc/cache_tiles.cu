@@ -36,6 +36,8 @@
 // on the device (plan_kernel), for the lengths are read there.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "cache_attn.cuh"
 
 namespace h3 {
@@ -203,7 +205,12 @@ struct PageMeta {
   float t;
   int plain;    // 64 valid keys, V scale in the range in which it goes into the exponent
 };
-constexpr float kPlainScale = 8.673617379884035e-19f;  // 2^-60: p vs >= 2^-126 for p >= 2^-66
+// V scales in [2^-60, 2^40] go into the exponent: p vs is then normal for p in [2^-66, 2^kStale].
+constexpr float kScaleLow = 8.673617379884035e-19f, kScaleHigh = 1099511627776.0f;
+// A score may exceed the running maximum by this much (log2 units) before the
+// maximum is brought up: probabilities, sums and O are floating point, so a stale
+// maximum costs no accuracy, and one pass over the scores is enough.
+constexpr float kStale = 60.0f;
 
 template <int D>
 struct TilesLayout {
@@ -312,11 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       const int sub = warp >> 2, r = tid & 127;  // r: row of the tile = TMEM lane
       const int pr = sub * 128 + r;
       const bool valid = pr < it.pairs;
-      const long long pair = it.pair0 + pr;
-      const int row = valid ? (int)(pair / p.group) : 0;
+      // pair pr of the tile: its query row and head
+      const int i0 = (int)(it.pair0 / p.group), g0 = (int)(it.pair0 % p.group) + (valid ? pr : 0);
+      const int row = i0 + g0 / p.group, head = it.hk * p.group + g0 % p.group;
       {
-        const uint16_t* src = p.q + (it.hk * p.group + (valid ? (int)(pair % p.group) : 0)) * p.q_head +
-                              (long long)(it.first + row) * p.q_row;
+        const uint16_t* src = p.q + head * p.q_head + (long long)(it.first + row) * p.q_row;
         uint8_t* dst = smem + L::kQ + sub * L::kBlockBytes + r * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -338,14 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         const uint32_t t_s = tmem + lane_addr + (uint32_t)(128 * sub);
         const uint32_t t_o = tmem + lane_addr + kTmemO + (uint32_t)(D * sub);
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
+        bool ok = true, warm = false;  // warm: every row of the warp has a running maximum
 
-        // the step's running maximum becomes at least mx; O and l follow
-        auto raise = [&](float mx) {
+        // The running maximum becomes at least mx - 8; O and l follow by the factor
+        // that is returned, a power of two.
+        auto raise = [&](float mx) -> float {
           const bool grow = mx > m + kRescaleThreshold;
           const bool rescale = grow && m > -INFINITY;
-          const float alpha = rescale ? ex2(m - mx) : 1.0f;
-          if (grow) m = mx;
+          const float up = rescale ? ceilf(mx - m) : 0.0f;
+          const float alpha = ex2(-up);
+          if (grow) m = rescale ? m + up : mx;
           if (__any_sync(kFull, rescale)) {
             l *= alpha;
 #pragma unroll 1
@@ -360,14 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
               tmem_st32(t_o + c * 32, y);
             }
           }
-        };
-        auto top64 = [&](const float (&x)[32], const float (&y)[32]) -> float {
-          float mp[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mp[i] = fmaxf(x[i], y[i]);
-#pragma unroll
-          for (int i = 4; i < 32; ++i) mp[i & 3] = max3f(mp[i & 3], x[i], y[i]);
-          return fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]);
+          return alpha;
         };
 
         for (int j = 0; ok && j < n; ++j) {
@@ -388,76 +390,114 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           if (plain) {
             float x[32], y[32];
             uint32_t pk[32];
-            auto fetch = [&](int col) {
+            auto load32 = [&](float (&to)[32], int col) {
               __syncwarp();
-              tmem_ld32f(t_s + col, x);
-              tmem_ld32f(t_s + col + 32, y);
-              tmem_landed(x);
-              tmem_landed(y);
+              tmem_ld32f(t_s + col, to);
             };
-            fetch(64);
-            float mx = top64(x, y) * pb.c - pen_b;
-            fetch(0);
-            mx = fmaxf(mx, top64(x, y) * pa.c - pen_a);
-            raise(mx);
-            auto probs = [&](const PageMeta& pg, float pen) {
+            auto top32 = [&](const float (&s)[32]) -> float {
+              float mp[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mp[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+              for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mp[e] = max3f(mp[e], s[i + e], s[i + 4 + e]);
+              return fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]);
+            };
+            auto probs32 = [&](const float (&s)[32], float off, float c, uint32_t* to) -> float {
+              return probs16_fast(s, off, c, to) + probs16_fast(s + 16, off, c, to + 8);
+            };
+            // one page with the running maximum as it is; false if a score exceeds it by 2^kStale
+            auto page = [&](int col, const PageMeta& pg, float pen, bool more) -> bool {
               const float off = pg.lv - m - pen;
-              float s0 = probs16_fast(x, off, pg.c, pk), s1 = probs16_fast(x + 16, off, pg.c, pk + 8);
-              s0 += probs16_fast(y, off, pg.c, pk + 16);
-              s1 += probs16_fast(y + 16, off, pg.c, pk + 24);
-              l = fmaf(s0 + s1, pg.iv, l);
+              tmem_landed(x);
+              load32(y, col + 32);
+              float top = top32(x), s = probs32(x, off, pg.c, pk);
+              tmem_landed(y);
+              if (more) load32(x, col + 64);
+              top = fmaxf(top, top32(y));
+              s += probs32(y, off, pg.c, pk + 16);
+              if (__any_sync(kFull, top * pg.c - pen > m + kStale)) return false;
+              l = fmaf(s, pg.iv, l);
+              __syncwarp();
+              tmem_st32(t_s + col / 2, pk);
+              return true;
             };
-            probs(pa, pen_a);
-            __syncwarp();
-            tmem_st32(t_s, pk);
-            fetch(64);
-            probs(pb, pen_b);
-            __syncwarp();
-            tmem_st32(t_s + 32, pk);
+            load32(x, 0);
+            const bool first = warm && page(0, pa, pen_a, true);  // the first page's probabilities are stored
+            warm = first && page(64, pb, pen_b, false);
+            if (!warm) {
+              // bring the maximum up first: over both pages, or over the second one when the first is stored
+              float mx = m;
+              tmem_landed(x);
+              for (int c = first ? 64 : 0; c < 128; c += 32) {
+                load32(x, c);
+                tmem_landed(x);
+                mx = fmaxf(mx, top32(x) * (c < 64 ? pa.c : pb.c) - (c < 64 ? pen_a : pen_b));
+              }
+              const float alpha = raise(mx);
+              if (first) {
+                uint32_t w[32];
+                tmem_ld32(t_s, w);
+                tmem_landed(w);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  w[i] = pack_bf16(__uint_as_float(w[i] << 16) * alpha, __uint_as_float(w[i] & 0xFFFF0000u) * alpha);
+                __syncwarp();
+                tmem_st32(t_s, w);
+              }
+              load32(x, first ? 64 : 0);
+              if (!first) page(0, pa, pen_a, true);
+              page(64, pb, pen_b, false);
+              warm = __all_sync(kFull, m > -INFINITY);
+            }
           } else {
-            // validity, visibility and penalty key by key
-            auto score = [&](float raw, int key, const PageMeta& pg, float pen) -> float {
-              if ((key & 63) >= pg.live || key0 + key >= lim) return -INFINITY;
-              if (kPen && pg.mode == 2) pen = block_penalty_log2(tq, times[key], p);
-              return raw * pg.c - pen;
+            // Validity, visibility and penalty key by key, in two passes.  Keys from
+            // `end` on (within the 32 of a load) are not seen; branch-free, as every
+            // lane has an end of its own.
+            auto scores32 = [&](float (&s)[32], int c, auto timed) {
+              const PageMeta& pg = c < 2 ? pa : pb;
+              const float pen = c < 2 ? pen_a : pen_b;
+              const int end = min(pg.live - (c & 1) * 32, lim - key0 - c * 32);
+              __syncwarp();
+              tmem_ld32f(t_s + c * 32, s);
+              tmem_landed(s);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float q = decltype(timed)::value ? block_penalty_log2(tq, times[c * 32 + i], p) : pen;
+                s[i] = i < end ? fmaf(s[i], pg.c, -q) : -INFINITY;
+              }
+            };
+            auto any_scores32 = [&](float (&s)[32], int c) {
+              if (kPen && (c < 2 ? pa.mode : pb.mode) == 2) scores32(s, c, std::true_type{});
+              else scores32(s, c, std::false_type{});
             };
             float mx = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              float x[32];
-              __syncwarp();
-              tmem_ld32f(t_s + c * 32, x);
-              tmem_landed(x);
-              const PageMeta& pg = c < 2 ? pa : pb;
-              const float pen = c < 2 ? pen_a : pen_b;
+              float s[32];
+              any_scores32(s, c);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, score(x[i], c * 32 + i, pg, pen));
+              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[i]);
             }
             raise(mx);
+            warm = __all_sync(kFull, m > -INFINITY);
             const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pk[32];
-              const PageMeta& pg = c == 0 ? pa : pb;
-              const float pen = c == 0 ? pen_a : pen_b;
+            for (int c = 0; c < 4; ++c) {
+              const float vs = c < 2 ? pa.vs : pb.vs;
+              float s[32];
+              uint32_t pk[16];
+              any_scores32(s, c);
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                float x[32];
-                __syncwarp();
-                tmem_ld32f(t_s + c * 64 + half * 32, x);
-                tmem_landed(x);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const int key = c * 64 + half * 32 + i;
-                  const float e0 = ex2(score(x[i], key, pg, pen) - base);
-                  const float e1 = ex2(score(x[i + 1], key + 1, pg, pen) - base);
-                  l += e0 + e1;
-                  // a scale that is not finite stays away from rows that do not see the key
-                  pk[half * 16 + i / 2] = pack_bf16(e0 == 0.0f ? 0.0f : e0 * pg.vs, e1 == 0.0f ? 0.0f : e1 * pg.vs);
-                }
+              for (int i = 0; i < 32; i += 2) {
+                const float e0 = ex2(s[i] - base), e1 = ex2(s[i + 1] - base);
+                l += e0 + e1;
+                // a scale that is not finite stays away from rows that do not see the key
+                pk[i / 2] = pack_bf16(e0 == 0.0f ? 0.0f : e0 * vs, e1 == 0.0f ? 0.0f : e1 * vs);
               }
               __syncwarp();
-              tmem_st32(t_s + c * 32, pk);
+              tmem_st16(t_s + c * 16, pk);
             }
           }
           tmem_wait_st();
@@ -470,6 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         if (ok) {
           tc_fence_after();
           const bool whole = n == it.steps;
+          const size_t at = (size_t)head * p.b.T + it.first + row;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           float* slot = whole ? nullptr : slot_of<D>(p, blockIdx.x, step0 > 0 ? 0 : 1);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -481,11 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 v = make_float4(x[i], x[i + 2], x[i + 1], x[i + 3]);
-                if (whole) store_cols(p, it.first, it.hk, pair, c * 32 + i, v, m, l);
+                if (whole) store_cols(p, at, c * 32 + i, v, inv);
                 else *reinterpret_cast<float4*>(slot + pr * D + c * 32 + i) = v;
               }
             }
           }
+          if (whole && valid) store_lse(p, at, m, l);
           if (!whole && valid) *reinterpret_cast<float2*>(slot + kTile * D + 2 * pr) = make_float2(m, l);
         }
         // a step left early may still have TMEM accesses in flight
@@ -572,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
             times[lane] = t0;
             times[lane + 32] = t1;
           }
-          pm.plain = live == kBlock && pm.mode != 2 && vs >= kPlainScale && vs < 1e30f;
+          pm.plain = live == kBlock && pm.mode != 2 && vs >= kScaleLow && vs <= kScaleHigh;
           if (lane == 0) reinterpret_cast<PageMeta*>(smem + L::kMeta)[2 * slot + page_of] = pm;
         }
         __syncwarp();
@@ -674,6 +717,7 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p
   if (it.start == u || it.start / share != c0) return;
   const long long c1 = (it.start + it.steps - 1) / share;
   const int r0 = blockIdx.y * 32;
+  const int i0 = (int)(it.pair0 / p.group), g0 = (int)(it.pair0 % p.group);
   for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
     const int r = r0 + i / (D / 4), col = i % (D / 4) * 4;
     if (r >= it.pairs) break;
@@ -691,7 +735,9 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p
       sum.x = sum.x * a + e * y.x, sum.y = sum.y * a + e * y.y;
       sum.z = sum.z * a + e * y.z, sum.w = sum.w * a + e * y.w;
     }
-    store_cols(p, it.first, it.hk, it.pair0 + r, col, sum, mm, ll);
+    const size_t at = (size_t)(it.hk * p.group + (g0 + r) % p.group) * p.b.T + it.first + i0 + (g0 + r) / p.group;
+    store_cols(p, at, col, sum, ll == 0.0f ? 0.0f : 1.0f / ll);
+    if (col == 0) store_lse(p, at, mm, ll);
   }
 }
 
