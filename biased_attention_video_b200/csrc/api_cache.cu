@@ -107,6 +107,7 @@ int h3attn_cache_append(const h3attn_cache* cache, const h3attn_batch* batch, co
   p.v_head = v_head_stride;
   p.v_row = v_row_stride;
   p.row_times = row_times;
+  p.minus_zero = -0.0f;
   p.status = static_cast<int*>(ws);
   return h3::launch_cache_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ECUDA;
 }

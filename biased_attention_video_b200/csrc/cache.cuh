@@ -42,6 +42,7 @@ struct AppendParams {
   long long k_head, k_row, v_head, v_row;  // strides in elements
   const float* row_times;
   int* status;
+  float minus_zero;  // -0, see mul2_rn
 };
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
 
@@ -106,64 +107,71 @@ __device__ __forceinline__ int seq_length(const BatchRef& r, int b, int* status)
 
 // Piece x of the call: the rows of one sequence that lie in one page.  Pieces
 // are counted sequence by sequence; sequence b's rows take the positions from
-// length[b] on.  Called by every thread of a block of NT threads; b = -1 when
-// the call has no piece x.
+// length[b] on.  b = -1 when the call has no piece x.
 struct Piece {
   int b, page_no, lo, hi;  // positions [lo, hi) of sequence b, inside its page page_no
   int row;                 // packed row of position lo
   int held;                // earlier rows of the page that stay
 };
-template <int NT>
+// Every warp finds the piece for itself (no barrier): a lane counts the pieces of
+// kSeqs consecutive sequences, all their loads issued together.
 __device__ __forceinline__ Piece find_piece(const BatchRef& r, int x, int* status) {
-  __shared__ int warp_sum[NT / 32], found[5];  // found: sequence, its start, rows, first packed row, piece in it
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found[0] = -1;
+  constexpr int kSeqs = 4;
+  const int lane = threadIdx.x & 31;
+  Piece p{};
+  p.b = -1;
   int base = 0;
-  for (int b0 = 0; b0 < r.B && base <= x; b0 += NT) {
-    const int b = b0 + tid;
-    int start = 0, n = 0, first = 0, cnt = 0;
-    if (b < r.B) {
-      const SeqRows s = seq_rows(r, b, status);
-      start = seq_length(r, b, status);
-      first = s.first;
-      n = min(s.n, r.max_pages * kBlock - start);
-      if (n < s.n) cache_report(status, kStatusData);
-      cnt = n > 0 ? (start + n - 1) / kBlock - start / kBlock + 1 : 0;
+  for (int b0 = 0; b0 < r.B && p.b < 0; b0 += 32 * kSeqs) {
+    int start[kSeqs], n[kSeqs], first[kSeqs], cnt[kSeqs], mine = 0;
+#pragma unroll
+    for (int e = 0; e < kSeqs; ++e) {
+      const int b = b0 + lane * kSeqs + e;
+      start[e] = n[e] = first[e] = cnt[e] = 0;
+      if (b < r.B) {
+        const SeqRows s = seq_rows(r, b, status);
+        start[e] = seq_length(r, b, status);
+        first[e] = s.first;
+        n[e] = min(s.n, r.max_pages * kBlock - start[e]);
+        if (n[e] < s.n) cache_report(status, kStatusData);
+        cnt[e] = n[e] > 0 ? (start[e] + n[e] - 1) / kBlock - start[e] / kBlock + 1 : 0;
+      }
+      mine += cnt[e];
     }
-    int incl = cnt;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += v;
     }
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int off = base;
+    int i = x - base - (incl - mine);  // the piece's number among this lane's
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, i >= 0 && i < mine);
+    if (who != 0u) {
+      const int from = __ffs(who) - 1;
+      int e_at = 0, s_at = 0, n_at = 0, f_at = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) off += warp_sum[w];
-      base += warp_sum[w];
+      for (int e = kSeqs - 1; e >= 0; --e) {  // the last sequence whose pieces begin at or before i
+        int before = 0;
+#pragma unroll
+        for (int k = 0; k < e; ++k) before += cnt[k];
+        if (i >= before && i < before + cnt[e]) {
+          e_at = e;
+          s_at = start[e];
+          n_at = n[e];
+          f_at = first[e];
+          i -= before;
+          break;
+        }
+      }
+      p.b = b0 + from * kSeqs + __shfl_sync(0xFFFFFFFFu, e_at, from);
+      const int begin = __shfl_sync(0xFFFFFFFFu, s_at, from);
+      const int end = begin + __shfl_sync(0xFFFFFFFFu, n_at, from);
+      p.page_no = begin / kBlock + __shfl_sync(0xFFFFFFFFu, i, from);
+      p.lo = max(begin, p.page_no * kBlock);
+      p.hi = min(end, (p.page_no + 1) * kBlock);
+      p.row = __shfl_sync(0xFFFFFFFFu, f_at, from) + p.lo - begin;
+      p.held = p.lo - p.page_no * kBlock;
     }
-    const int i = x - (off + incl - cnt);
-    if (i >= 0 && i < cnt) {
-      found[0] = b;
-      found[1] = start;
-      found[2] = n;
-      found[3] = first;
-      found[4] = i;
-    }
-  }
-  __syncthreads();
-  Piece p{};
-  p.b = found[0];
-  if (p.b >= 0) {
-    const int start = found[1], end = start + found[2];
-    p.page_no = start / kBlock + found[4];
-    p.lo = max(start, p.page_no * kBlock);
-    p.hi = min(end, (p.page_no + 1) * kBlock);
-    p.row = found[3] + p.lo - start;
-    p.held = p.lo - p.page_no * kBlock;
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
   return p;
 }
