@@ -64,6 +64,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A kernel launched by launch_after may start while the one before it in the
+// stream still runs: launch_dependents() in that one says from when on, and
+// wait_dependency() in this one waits until all of that one's work is done and
+// seen.  Every block waits, also one with nothing to do, so that the kernels
+// behind never start before the first one's end.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+inline cudaError_t launch_after(void (*kernel)(CacheAttnParams), dim3 grid, int threads, int smem, cudaStream_t stream,
+                                const CacheAttnParams& p) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, p);
+}
+
 // Columns [col, col + 4) of output row `at` (head T + packed row) from unnormalised v; inv = 1 / sum, 0 for no key.
 __device__ __forceinline__ void store_cols(const CacheAttnParams& p, size_t at, int col, float4 v, float inv) {
   *reinterpret_cast<uint2*>(p.o + at * p.c.d + col) =

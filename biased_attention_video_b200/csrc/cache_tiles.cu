@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const CacheAttnParams p) {
   __shared__ long long units[32];
   __shared__ long long before;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  launch_dependents();
   if (threadIdx.x == 0) {
     before = 0;
     p.base[0] = 0;
@@ -246,6 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   Item* item_slot = reinterpret_cast<Item*>(smem + L::kItem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  launch_dependents();
+  wait_dependency();
   const long long total = p.base[p.b.B], share = share_of(total);
   const long long u0 = blockIdx.x * share, u1 = min(total, u0 + share);
   if (u0 >= u1) return;
@@ -705,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
 template <int D>
 __global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p) {
   __shared__ Item item;
+  wait_dependency();
   const long long total = p.base[p.b.B], share = share_of(total);
   const long long c0 = blockIdx.x, u = (c0 + 1) * share;
   if (u >= total) return;
@@ -749,10 +753,8 @@ cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, 1024, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kernel<<<kGrid, kThreads, bytes, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  join_tiles_kernel<D><<<dim3(kGrid - 1, kTile / 32), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  if ((e = launch_after(kernel, dim3(kGrid), kThreads, bytes, stream, p)) != cudaSuccess) return e;
+  return launch_after(join_tiles_kernel<D>, dim3(kGrid - 1, kTile / 32), 256, 0, stream, p);
 }
 
 }  // namespace
