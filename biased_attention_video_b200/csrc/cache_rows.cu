@@ -39,15 +39,19 @@ namespace {
 
 using namespace sm;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kKeys = 16;    // keys of a granule
-constexpr int kStages = 3;
+constexpr int kWarps = 6, kThreads = 32 * kWarps;
+constexpr int kKeys = 32;    // keys of a granule
+constexpr int kM = kKeys / 16;
+constexpr int kStages = 2;
 constexpr int kJoinWarps = 16;
 constexpr float kRaise = 3.0f;   // log2 units: a score this far above the running maximum raises it
 constexpr float kShift = 12.0f;  // a probability is 2^kShift at the running maximum: at most 2^15 in fp16
 constexpr int kBlocksPerSm = 2;
 constexpr int kGrid = 148 * kBlocksPerSm;
-constexpr int kMinShare = kWarps * kKeys / kBlock;  // pages: one granule for every warp
+// What beginning and ending an item costs a block, in pages: it counts in the
+// line, so that a block that gets many short sequences gets fewer pages.
+constexpr int kItemCost = 3;
+constexpr int kMinShare = kItemCost + 1;
 
 template <int D, int NT>
 struct RowsLayout {
@@ -57,7 +61,12 @@ struct RowsLayout {
   static constexpr int kStage = kMeta + 16 + kKeys * 4;
   static constexpr int kPitch = D + 4;              // floats of one row of the warps' results
   static constexpr int kResult = kRows * kPitch * 4;
-  static constexpr int kRing = kStages * kStage > kResult ? kStages * kStage : kResult;
+  // A warp's results lie behind its ring, so that the next item's first granules
+  // load while the warps' results are joined; over it where that would cost a
+  // block per SM.
+  static constexpr bool kBehind = false;
+  static constexpr int kRes = kBehind ? kStages * kStage : 0;
+  static constexpr int kRing = kBehind ? kRes + kResult : kStages * kStage > kResult ? kStages * kStage : kResult;
   static constexpr int kQ = kWarps * kRing;         // Q fragments: [D / 16][NT][32] uint2
   static constexpr int kQScale = kQ + D / 16 * NT * 256;  // [R] powers of two
   static constexpr int kMl = kQScale + kRows * 4;
@@ -105,8 +114,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // ---------------------------------------------------------------- the line
 
-// Sequence b's share of the line: tiles x K/V heads x pages (at least one page,
-// so that a sequence without cached rows still gets its rows written).
+// Sequence b's share of the line: tiles x K/V heads x (kItemCost + pages), with
+// one page at least, so that a sequence without cached rows still gets its rows
+// written.
 struct Seq {
   int first, n, len, pages;
   long long tiles, units;
@@ -120,7 +130,7 @@ __device__ __forceinline__ Seq load_seq(const CacheAttnParams& p, int b) {
   s.len = seq_length(p.b, b, p.status);
   s.pages = max(1, (s.len + kBlock - 1) / kBlock);
   s.tiles = ((long long)s.n * p.group + R - 1) / R;
-  s.units = s.tiles * p.c.H * s.pages;
+  s.units = s.tiles * p.c.H * (s.pages + kItemCost);
   return s;
 }
 
@@ -196,9 +206,71 @@ __device__ __forceinline__ long long share_of(long long total) {
   return even > kMinShare ? even : kMinShare;
 }
 
-// Output row (head T + packed row) of a pair of the sequence's list.
-__device__ __forceinline__ size_t row_of(const CacheAttnParams& p, const Seq& s, int hk, long long pair) {
-  return (size_t)(hk * p.group + (int)(pair % p.group)) * p.b.T + s.first + (int)(pair / p.group);
+// A block's piece of an item: pages [page0, page1) of one tile of one sequence
+// and K/V head.  The first kItemCost + 1 units of an item stand for its first
+// page; a piece that begins inside them has no page if there is only that one.
+struct Piece1 {
+  int b, hk, page0, page1, pairs;
+  int i0, g0;              // query row and head of the group of the tile's first pair
+  long long pair0, start;  // the tile's first pair; the line before the item
+  long long end;           // the line up to the piece's end
+  long long before;        // the line before the sequence
+  Seq s;
+  __device__ __forceinline__ int units() const { return s.pages + kItemCost; }
+  __device__ __forceinline__ void cut(long long u, long long u1) {
+    const int x0 = (int)(u - start), x1 = (int)min((long long)units(), u1 - start);
+    page0 = x0 == 0 ? 0 : max(1, x0 - kItemCost);
+    page1 = x1 == units() ? s.pages : max(1, x1 - kItemCost);
+    end = start + x1;
+  }
+};
+// The piece that unit u of the line begins, inside sequence s (`before` it).
+template <int R>
+__device__ __forceinline__ Piece1 piece_at(const CacheAttnParams& p, int b, const Seq& s, long long before, long long u,
+                                           long long u1) {
+  Piece1 w;
+  w.b = b;
+  w.s = s;
+  w.before = before;
+  const long long d = u - before;
+  const int units = w.units();
+  const long long item = d < 0x7FFFFFFF ? (long long)((unsigned)d / (unsigned)units) : d / units;
+  const long long tile = item < 0x7FFFFFFF ? (long long)((unsigned)item / (unsigned)p.c.H) : item / p.c.H;
+  w.hk = (int)(item - tile * p.c.H);
+  w.start = before + item * units;
+  w.cut(u, u1);
+  w.pair0 = tile * R;
+  w.i0 = w.g0 = 0;
+  if (tile > 0) {
+    w.i0 = (int)(w.pair0 / p.group);
+    w.g0 = (int)(w.pair0 - (long long)w.i0 * p.group);
+  }
+  w.pairs = (int)min((long long)R, (long long)s.n * p.group - w.pair0);
+  return w;
+}
+// The piece after w, which ends its item; u: its first unit.
+template <int R>
+__device__ __forceinline__ Piece1 piece_after(const CacheAttnParams& p, const Piece1& w, long long u, long long u1) {
+  if (u < w.before + w.s.units && w.hk + 1 < p.c.H) {  // the next K/V head of the same tile
+    Piece1 v = w;
+    ++v.hk;
+    v.start = u;
+    v.cut(u, u1);
+    return v;
+  }
+  int b = w.b;
+  Seq s = w.s;
+  long long before = w.before;
+  while (u >= before + s.units) {
+    before += s.units;
+    s = load_seq<R>(p, ++b);
+  }
+  return piece_at<R>(p, b, s, before, u, u1);
+}
+// Output row (head T + packed row) of pair r of the tile.
+__device__ __forceinline__ size_t row_of(const CacheAttnParams& p, const Piece1& w, int r) {
+  const unsigned q = (unsigned)(w.g0 + r), i = q / (unsigned)p.group, g = q - i * (unsigned)p.group;
+  return (size_t)(w.hk * p.group + (int)g) * p.b.T + w.s.first + w.i0 + (int)i;
 }
 
 // Slot of partial results: unnormalised O [R][D], then (maximum, sum) [R].
@@ -228,46 +300,79 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
   const long long u0 = blockIdx.x * share, u1 = min(total, u0 + share);
   if (u0 >= u1) return;
   long long before;
-  int b = line.find(p, u0, &before);
-  Seq s = load_seq<R>(p, b);
+  const int b0 = line.find(p, u0, &before);
+  Piece1 w = piece_at<R>(p, b0, load_seq<R>(p, b0), before, u0, u1);
+  if (w.page0 >= w.page1) {  // the rest of an item of one page, which the block before has
+    if (w.end >= u1) return;
+    w = piece_after<R>(p, w, w.end, u1);
+  }
 
-  for (long long u = u0; u < u1;) {
-    while (u >= before + s.units) {
-      before += s.units;
-      s = load_seq<R>(p, ++b);
+  // this warp's granules of the piece: keys first, first + kWarps * kKeys, ... < end
+  int end, first, steps;
+  auto begin = [&]() {
+    end = min(w.s.len, w.page1 * kBlock);
+    first = w.page0 * kBlock + warp * kKeys;
+    steps = first < end ? (end - first + kWarps * kKeys - 1) / (kWarps * kKeys) : 0;
+  };
+  auto issue = [&](int i) {
+    if (i < steps) {
+      const int key = first + i * (kWarps * kKeys);
+      const int page = page_id(p.c, p.b, w.b, key / kBlock, p.status);
+      const uint32_t st = ring_a + i % kStages * L::kStage;
+      if (page >= 0) {
+        const size_t at = (size_t)page * p.c.H + w.hk;
+        const size_t off = at * kBlock * D + (size_t)(key % kBlock) * D;
+#pragma unroll
+        for (int c = 0; c < kKeys * D / 512; ++c) {
+          const int idx = c * 32 + lane, row = idx / (D / 16), ch = idx % (D / 16);
+          const int ck = D == 128 ? ch ^ ((row & 1) << 2) : ch;
+          const int cv = D == 128 ? ch ^ ((row >> 1 & 3) << 1) : ch ^ (row >> 1 & 3);
+          cp_async16(st + row * D + ck * 16, p.c.k + off + idx * 16);
+          cp_async16(st + L::kV + row * D + cv * 16, p.c.v + off + idx * 16);
+        }
+        if (lane == 0) cp_async4(st + L::kMeta, p.c.k_scale + at);
+        if (lane == 1) cp_async4(st + L::kMeta + 4, p.c.v_scale + at);
+        if (kPen && lane >= 8 && lane < 8 + kKeys / 4)
+          cp_async16(st + L::kMeta + 16 + (lane - 8) * 16,
+                     p.c.times + (size_t)page * kBlock + key % kBlock + (lane - 8) * 4);
+      }
+      if (lane == 2)
+        *reinterpret_cast<int*>(ring + i % kStages * L::kStage + L::kMeta + 8) = page >= 0 ? min(kKeys, end - key) : 0;
     }
-    // item: tile by tile, K/V head by K/V head, page by page
-    const long long item = (u - before) / s.pages, item_u = before + item * s.pages;
-    const int hk = (int)(item % p.c.H);
-    const long long pair0 = item / p.c.H * R;
-    const int page0 = (int)(u - item_u), page1 = (int)min((long long)s.pages, u1 - item_u);
-    const int pairs = (int)min((long long)R, (long long)s.n * p.group - pair0);
+    cp_async_commit();
+  };
+  // Q of the piece's tile (8 columns n = pairs; k = the columns of a word of codes)
+  uint4 qw[D / 32];
+  auto load_q = [&]() {
+    const int r = (kQRegs ? 0 : warp * 8) + g;
+    const uint16_t* src = nullptr;
+    if ((kQRegs || warp < NT) && r < w.pairs) {
+      const unsigned q = (unsigned)(w.g0 + r), i = q / (unsigned)p.group, gg = q - i * (unsigned)p.group;
+      src = p.q + (w.hk * p.group + (int)gg) * p.q_head + (long long)(w.s.first + w.i0 + (int)i) * p.q_row + t * 16;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      qw[c] = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src + c / 2 * 64) + (c & 1)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  begin();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  load_q();
 
-    // Q fragments of the item (8 columns n = pairs; k = the columns of a word of codes)
+  while (true) {
     __syncthreads();  // the last item's results and fragments are read
     uint32_t qf[kQRegs ? 2 * kJ : 1];
     if (kQRegs || warp < NT) {
       const int r = (kQRegs ? 0 : warp * 8) + g;
-      const uint16_t* src = nullptr;
-      if (r < pairs) {
-        const long long pair = pair0 + r;
-        const int h = hk * p.group + (int)(pair % p.group);
-        src = p.q + h * p.q_head + (s.first + pair / p.group) * p.q_row;
-      }
       float y[D / 4], top = 0.0f;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (src != nullptr) {
-          w[0] = __ldg(reinterpret_cast<const uint4*>(src + c * 64 + t * 16));
-          w[1] = __ldg(reinterpret_cast<const uint4*>(src + c * 64 + t * 16) + 1);
-        }
-        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t x[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[16 * c + 2 * i] = __uint_as_float(x[i] << 16);
-          y[16 * c + 2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-          top = fmaxf(top, fmaxf(fabsf(y[16 * c + 2 * i]), fabsf(y[16 * c + 2 * i + 1])));
+        for (int i = 0; i < 4; ++i) {
+          y[8 * c + 2 * i] = __uint_as_float(x[i] << 16);
+          y[8 * c + 2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+          top = fmaxf(top, fmaxf(fabsf(y[8 * c + 2 * i]), fabsf(y[8 * c + 2 * i + 1])));
         }
       }
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
@@ -291,20 +396,20 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
     }
     __syncthreads();
     // what this lane's pairs may see, and their times
-    int lim[NT][2], lim_all = s.len;
+    int lim[NT][2], lim_all = w.s.len;
     float tq[NT][2], qs[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * x + 2 * t + e;
-        lim[x][e] = s.len;
+        lim[x][e] = w.s.len;
         tq[x][e] = NAN;
         qs[x][e] = reinterpret_cast<const float*>(smem + L::kQScale)[r] * p.scale_log2;
-        if (r < pairs) {
-          const int i = (int)((pair0 + r) / p.group);
-          if (p.causal) lim[x][e] = min(s.len, max(0, s.len - s.n + i + 1));
-          if (kPen) tq[x][e] = __ldg(p.q_times + s.first + i);
+        if (r < w.pairs) {
+          const int i = w.i0 + (int)((unsigned)(w.g0 + r) / (unsigned)p.group);
+          if (p.causal) lim[x][e] = min(w.s.len, max(0, w.s.len - w.s.n + i + 1));
+          if (kPen) tq[x][e] = __ldg(p.q_times + w.s.first + i);
         }
         lim_all = min(lim_all, lim[x][e]);
       }
@@ -313,40 +418,6 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
     float o[NT][kJ][4] = {}, m[NT][2], l[NT][2] = {};
 #pragma unroll
     for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY;
-
-    const int end = min(s.len, page1 * kBlock);
-    const int first = page0 * kBlock + warp * kKeys;  // keys first, first + kWarps * kKeys, ...
-    const int steps = first < end ? (end - first + kWarps * kKeys - 1) / (kWarps * kKeys) : 0;
-
-    auto issue = [&](int i) {
-      if (i < steps) {
-        const int key = first + i * (kWarps * kKeys);
-        const int page = page_id(p.c, p.b, b, key / kBlock, p.status);
-        const uint32_t st = ring_a + i % kStages * L::kStage;
-        if (page >= 0) {
-          const size_t at = (size_t)page * p.c.H + hk;
-          const size_t off = at * kBlock * D + (size_t)(key % kBlock) * D;
-#pragma unroll
-          for (int c = 0; c < kKeys * D / 512; ++c) {
-            const int idx = c * 32 + lane, row = idx / (D / 16), ch = idx % (D / 16);
-            const int ck = D == 128 ? ch ^ ((row & 1) << 2) : ch;
-            const int cv = D == 128 ? ch ^ ((row >> 1 & 3) << 1) : ch ^ (row >> 1 & 3);
-            cp_async16(st + row * D + ck * 16, p.c.k + off + idx * 16);
-            cp_async16(st + L::kV + row * D + cv * 16, p.c.v + off + idx * 16);
-          }
-          if (lane == 0) cp_async4(st + L::kMeta, p.c.k_scale + at);
-          if (lane == 1) cp_async4(st + L::kMeta + 4, p.c.v_scale + at);
-          if (kPen && lane >= 8 && lane < 8 + kKeys / 4)
-            cp_async16(st + L::kMeta + 16 + (lane - 8) * 16,
-                       p.c.times + (size_t)page * kBlock + key % kBlock + (lane - 8) * 4);
-        }
-        if (lane == 2)
-          *reinterpret_cast<int*>(ring + i % kStages * L::kStage + L::kMeta + 8) = page >= 0 ? min(kKeys, end - key) : 0;
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     for (int i = 0; i < steps; ++i) {
       cp_async_wait<kStages - 2>();
@@ -360,58 +431,75 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
       const float ks = meta[0], vs = meta[1], lv = log2_approx(vs), iv = vs < 3.0e38f ? rcp_approx(vs) : 1.0f;
       const int key = first + i * (kWarps * kKeys);
 
-      // S^T: 16 keys x 8 NT pairs
-      float acc[NT][4] = {};
+      // S^T: kKeys keys x 8 NT pairs
+      float acc[kM][NT][4] = {};
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const int ch = D == 128 ? (4 * c + t) ^ ((g & 1) << 2) : t;
-        const uint4 wa = lds128(st + g * D + ch * 16), wb = lds128(st + (g + 8) * D + ch * 16);
-        const uint32_t ra[4] = {wa.x, wa.y, wa.z, wa.w}, rb[4] = {wb.x, wb.y, wb.z, wb.w};
+      for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t a0 = widen2h(ra[w]), a1 = widen2h(rb[w]), a2 = widen2h(ra[w] >> 8), a3 = widen2h(rb[w] >> 8);
+        for (int c = 0; c < D / 64; ++c) {
+          const uint32_t a = st + (16 * mt + g) * D + (D == 128 ? (4 * c + t) ^ ((g & 1) << 2) : t) * 16;
+          const uint4 wa = lds128(a), wb = lds128(a + 8 * D);
+          const uint32_t ra[4] = {wa.x, wa.y, wa.z, wa.w}, rb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            uint2 f;
-            if constexpr (kQRegs) f = make_uint2(qf[2 * (4 * c + w)], qf[2 * (4 * c + w) + 1]);
-            else f = lds64(q_a + (((4 * c + w) * NT + x) * 32 + lane) * 8);
-            mma_f16(acc[x], a0, a1, a2, a3, f.x, f.y);
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const uint32_t a0 = widen2h(ra[i4]), a1 = widen2h(rb[i4]);
+            const uint32_t a2 = widen2h(ra[i4] >> 8), a3 = widen2h(rb[i4] >> 8);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              uint2 f;
+              if constexpr (kQRegs) f = make_uint2(qf[2 * (4 * c + i4)], qf[2 * (4 * c + i4) + 1]);
+              else f = lds64(q_a + (((4 * c + i4) * NT + x) * 32 + lane) * 8);
+              mma_f16(acc[mt][x], a0, a1, a2, a3, f.x, f.y);
+            }
           }
         }
+      // scores times V scales in log2 units: [x][0], [x][1] key g, [x][2], [x][3] key g + 8 of a 16
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        const float c0 = qs[x][0] * ks, c1 = qs[x][1] * ks;
+#pragma unroll
+        for (int mt = 0; mt < kM; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = fmaf(acc[mt][x][e], e & 1 ? c1 : c0, lv);
+            if (kPen) {
+              const float dt = fabsf(tq[x][e & 1] - meta[4 + 16 * mt + g + (e >> 1) * 8]);
+              const float ex = fmaxf(dt - p.window, 0.0f) * p.inv_falloff;
+              v -= fminf(p.strength_log2 * ex * ex, p.cap_log2);
+            }
+            acc[mt][x][e] = v;
+          }
       }
-      // scores times V scales in log2 units: [x][0], [x][1] key g, [x][2], [x][3] key g + 8
-      float over = -1.0f;  // whether one lies kRaise above its pair's running maximum
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = fmaf(acc[x][e], qs[x][e & 1] * ks, lv);
-          if (kPen) {
-            const float ex = fmaxf(fabsf(tq[x][e & 1] - meta[4 + g + (e >> 1) * 8]) - p.window, 0.0f) * p.inv_falloff;
-            v -= fminf(p.strength_log2 * ex * ex, p.cap_log2);
-          }
-          acc[x][e] = v;
-        }
       if (key + live > lim_all || live < kKeys) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = g + (e >> 1) * 8;
-            if (kk >= live || key + kk >= lim[x][e & 1]) acc[x][e] = -INFINITY;
-          }
-      }
+          for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        if (fmaxf(acc[x][0], acc[x][2]) > m[x][0] + kRaise) over = 1.0f;
-        if (fmaxf(acc[x][1], acc[x][3]) > m[x][1] + kRaise) over = 1.0f;
+            for (int e = 0; e < 4; ++e) {
+              const int kk = 16 * mt + g + (e >> 1) * 8;
+              if (kk >= live || key + kk >= lim[x][e & 1]) acc[mt][x][e] = -INFINITY;
+            }
       }
-      if (__any_sync(kFull, over > 0.0f)) {
+      // a score kRaise above its pair's running maximum raises it
+      bool over = false;
+      float top[NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(acc[0][x][e], acc[0][x][e + 2]);
+#pragma unroll
+          for (int mt = 1; mt < kM; ++mt) mx = max3f(mx, acc[mt][x][e], acc[mt][x][e + 2]);
+          top[x][e] = mx;
+          over = over || mx > m[x][e] + kRaise;
+        }
+      if (__any_sync(kFull, over)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(acc[x][e], acc[x][e + 2]);
+            float mx = top[x][e];
 #pragma unroll
             for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, q));
             const float mn = fmaxf(m[x][e], mx);
@@ -425,47 +513,66 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
             }
           }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[kM][NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
         const float m0 = (m[x][0] == -INFINITY ? 0.0f : m[x][0]) - kShift;
         const float m1 = (m[x][1] == -INFINITY ? 0.0f : m[x][1]) - kShift;
-        const float p0 = ex2(acc[x][0] - m0), p1 = ex2(acc[x][1] - m1);
-        const float p2 = ex2(acc[x][2] - m0), p3 = ex2(acc[x][3] - m1);
-        l[x][0] = fmaf(p0 + p2, iv, l[x][0]);
-        l[x][1] = fmaf(p1 + p3, iv, l[x][1]);
-        pb[x][0] = transpose8x8(pack_f16(p0, p1));
-        pb[x][1] = transpose8x8(pack_f16(p2, p3));
-      }
-      // O^T += V^T P^T: this lane's keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, its columns from g D / 8 on
-      uint32_t v[4][D / 32];
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 2 * t + (r & 1) + (r >> 1) * 8;
-        const uint32_t a = st + L::kV + row * D;
-        if constexpr (D == 128) {
-          const uint4 w = lds128(a + ((g ^ ((row >> 1 & 3) << 1)) << 4));
-          v[r][0] = w.x, v[r][1] = w.y, v[r][2] = w.z, v[r][3] = w.w;
-        } else {
-          const uint2 w = lds64(a + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
-          v[r][0] = w.x, v[r][1] = w.y;
+        for (int mt = 0; mt < kM; ++mt) {
+          const float p0 = ex2(acc[mt][x][0] - m0), p1 = ex2(acc[mt][x][1] - m1);
+          const float p2 = ex2(acc[mt][x][2] - m0), p3 = ex2(acc[mt][x][3] - m1);
+          s0 += p0 + p2;
+          s1 += p1 + p3;
+          pb[mt][x][0] = transpose8x8(pack_f16(p0, p1));
+          pb[mt][x][1] = transpose8x8(pack_f16(p2, p3));
+        }
+        l[x][0] = fmaf(s0, iv, l[x][0]);
+        l[x][1] = fmaf(s1, iv, l[x][1]);
+      }
+      // O^T += V^T P^T: this lane's keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of a 16, its columns from g D / 8 on
+#pragma unroll
+      for (int mt = 0; mt < kM; ++mt) {
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 2 * t + (r & 1) + (r >> 1) * 8;
+          const uint32_t a = st + L::kV + (16 * mt + row) * D;
+          if constexpr (D == 128) {
+            const uint4 x = lds128(a + ((g ^ ((row >> 1 & 3) << 1)) << 4));
+            v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+          } else {
+            const uint2 x = lds64(a + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
+            v[r][0] = x.x, v[r][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+          const uint32_t ab = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel);
+          const uint32_t cd = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
+          const uint32_t a0 = widen2h(ab), a1 = widen2h(ab >> 8), a2 = widen2h(cd), a3 = widen2h(cd >> 8);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) mma_f16(o[x][j], a0, a1, a2, a3, pb[mt][x][0], pb[mt][x][1]);
         }
       }
+    }
+    __syncwarp();  // the ring is read
+
+    // on to the next piece: its first granules and its Q load while this one is joined
+    const Piece1 done = w;
+    const long long u = w.end;
+    const bool more = u < u1;
+    if (more) {
+      w = piece_after<R>(p, w, u, u1);
+      begin();
+      if constexpr (L::kBehind) {
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-        const uint32_t ab = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel);
-        const uint32_t cd = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
-        const uint32_t a0 = widen2h(ab), a1 = widen2h(ab >> 8), a2 = widen2h(cd), a3 = widen2h(cd >> 8);
-#pragma unroll
-        for (int x = 0; x < NT; ++x) mma_f16(o[x][j], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+        for (int i = 0; i < kStages - 1; ++i) issue(i);
       }
     }
-    cp_async_wait<0>();
-    __syncwarp();
-
-    // the warps' results, over their own rings
-    float* res = reinterpret_cast<float*>(ring);
+    float* res = reinterpret_cast<float*>(ring + L::kRes);
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -478,26 +585,27 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
         for (int j = 0; j < kJ; ++j)
           *reinterpret_cast<float2*>(res + r * L::kPitch + g * (D / 8) + 2 * j) = make_float2(o[x][j][e], o[x][j][e + 2]);
       }
+    if (more) load_q();
     __syncthreads();
-    const bool whole = page0 == 0 && page1 == s.pages;
-    float* slot = whole ? nullptr : slot_of<D, R>(p, blockIdx.x, page0 > 0 ? 0 : 1);
+    const bool whole = done.page0 == 0 && done.page1 == done.s.pages;
+    float* slot = whole ? nullptr : slot_of<D, R>(p, blockIdx.x, done.page0 > 0 ? 0 : 1);
     for (int i = tid; i < R * (D / 4); i += kThreads) {
       const int r = i / (D / 4), col = i % (D / 4) * 4;
-      if (r >= pairs) break;
+      if (r >= done.pairs) break;
       float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * R + r].x);
+      for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, ml[x * R + r].x);
       float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 x = ml[w * R + r];
-        const float a = x.x == -INFINITY ? 0.0f : ex2(x.x - mm);
-        const float4 y = *reinterpret_cast<const float4*>(smem + w * L::kRing + (r * L::kPitch + col) * 4);
-        ll += a * x.y;
+      for (int x = 0; x < kWarps; ++x) {
+        const float2 v = ml[x * R + r];
+        const float a = v.x == -INFINITY ? 0.0f : ex2(v.x - mm);
+        const float4 y = *reinterpret_cast<const float4*>(smem + x * L::kRing + L::kRes + (r * L::kPitch + col) * 4);
+        ll += a * v.y;
         sum.x += a * y.x, sum.y += a * y.y, sum.z += a * y.z, sum.w += a * y.w;
       }
       if (whole) {
-        const size_t at = row_of(p, s, hk, pair0 + r);
+        const size_t at = row_of(p, done, r);
         store_cols(p, at, col, sum, ll == 0.0f ? 0.0f : 1.0f / ll);
         if (col == 0) store_lse(p, at, mm, ll);
       } else {
@@ -505,86 +613,92 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
         if (col == 0) *reinterpret_cast<float2*>(slot + R * D + 2 * r) = make_float2(mm, ll);
       }
     }
-    u = item_u + page1;
+    if (!more) break;
+    if constexpr (!L::kBehind) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(i);
+    }
   }
+  cp_async_wait<0>();
 }
 
-// Joins the items that several blocks share: block x looks at the border
-// between the stretches x and x + 1 and joins the item that lies across it, if
-// it is that item's first border.
-//
-// kWays warps share a pair's slots; a lane holds D / 32 columns.
+// Joins the items that several blocks share: block x stands for the border
+// between the stretches x and x + 1 and works on the item that lies across it;
+// the blocks of an item's borders take its pairs in turn, and a block's warps
+// share a pair's slots.  A lane holds D / 32 columns.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const CacheAttnParams p) {
-  constexpr int R = 8 * NT, kWays = kJoinWarps > R ? kJoinWarps / R : 1, kCols = D / 32;
+  constexpr int R = 8 * NT, kCols = D / 32;
   using Cols = typename std::conditional<kCols == 4, float4, float2>::type;
-  __shared__ float part[kWays > 1 ? kJoinWarps : 1][D + 2];
+  __shared__ float part[kJoinWarps][D + 2];
   const Line<R, 32 * kJoinWarps> line(p);
   const long long total = line.total, share = share_of(total);
-  const long long c0 = blockIdx.x, u = (c0 + 1) * share;
+  const long long u = (blockIdx.x + 1) * share;
   if (u >= total) {
     wait_dependency();
     return;
   }
   long long before;
   const int b = line.find(p, u, &before);
-  const Seq s = load_seq<R>(p, b);
-  const long long item = (u - before) / s.pages, lo = before + item * s.pages, hi = lo + s.pages;
+  const Piece1 w = piece_at<R>(p, b, load_seq<R>(p, b), before, u, total);
   wait_dependency();
-  if (lo == u || lo / share != c0) return;
-  const int n = (int)((hi - 1) / share - c0) + 1;  // slots
-  const int hk = (int)(item % p.c.H);
-  const long long pair0 = item / p.c.H * R;
-  const int pairs = (int)min((long long)R, (long long)s.n * p.group - pair0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = warp % kWays;
+  if (w.start == u || w.s.pages == 1) return;  // the border lies between two items, or one block has all of it
+  const long long c0 = w.start / share;
+  const int n = (int)((w.start + w.units() - 1) / share - c0) + 1;    // slots: n - 1 borders
+  const int turn = (int)(blockIdx.x - c0);
+  const int rows = turn < w.pairs ? (w.pairs - turn + n - 2) / (n - 1) : 0;  // pairs turn, turn + n - 1, ...
+  const int ways = rows > 0 ? max(1, kJoinWarps / rows) : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, way = warp % ways;
   auto slot = [&](int c) { return slot_of<D, R>(p, c0 + c, c == 0 ? 1 : 0); };
-  for (int r = warp / kWays; r < R; r += kJoinWarps / kWays) {
+  for (int k0 = 0; k0 < rows; k0 += kJoinWarps / ways) {
+    const int k = k0 + warp / ways, r = turn + k * (n - 1);
+    const bool mine = k < rows && warp / ways < kJoinWarps / ways;
     float mm = -INFINITY, ll = 0.0f, sum[kCols] = {};
-    if (r < pairs)
-      for (int c = way; c < n; c += 32 * kWays) {  // 32 slots at a time, a lane for each
-        const int mine = c + lane * kWays;
-        const float2 x = mine < n ? *reinterpret_cast<const float2*>(slot(mine) + R * D + 2 * r)
-                                  : make_float2(-INFINITY, 0.0f);
+    if (mine)
+      for (int c = way; c < n; c += 32 * ways) {  // 32 slots at a time, a lane for each
+        const int at = c + lane * ways;
+        const float2 x = at < n ? *reinterpret_cast<const float2*>(slot(at) + R * D + 2 * r)
+                                : make_float2(-INFINITY, 0.0f);
         float mn = fmaxf(mm, x.x);
 #pragma unroll
         for (int q = 16; q > 0; q >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, q));
-        const float base = mn == -INFINITY ? 0.0f : mn, a = ex2(mm - base), w = ex2(x.x - base);
-        float lw = w * x.y;
+        const float base = mn == -INFINITY ? 0.0f : mn, a = ex2(mm - base), e_c = ex2(x.x - base);
+        float lw = e_c * x.y;
 #pragma unroll
         for (int q = 16; q > 0; q >>= 1) lw += __shfl_xor_sync(kFull, lw, q);
         mm = mn;
         ll = ll * a + lw;
 #pragma unroll
         for (int e = 0; e < kCols; ++e) sum[e] *= a;
-        const int live = min(32, (n - c + kWays - 1) / kWays);
+        const int live = min(32, (n - c + ways - 1) / ways);
 #pragma unroll 8
-        for (int k = 0; k < live; ++k) {
-          const float wk = __shfl_sync(kFull, w, k);
-          const Cols y = *(reinterpret_cast<const Cols*>(slot(c + k * kWays) + r * D) + lane);
+        for (int q = 0; q < live; ++q) {
+          const float wq = __shfl_sync(kFull, e_c, q);
+          const Cols y = *(reinterpret_cast<const Cols*>(slot(c + q * ways) + r * D) + lane);
           const float* yy = reinterpret_cast<const float*>(&y);
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) sum[e] = fmaf(wk, yy[e], sum[e]);
+          for (int e = 0; e < kCols; ++e) sum[e] = fmaf(wq, yy[e], sum[e]);
         }
       }
-    if constexpr (kWays > 1) {
+    if (ways > 1) {
+      __syncthreads();
 #pragma unroll
       for (int e = 0; e < kCols; ++e) part[warp][lane * kCols + e] = sum[e];
       if (lane == 0) part[warp][D] = mm, part[warp][D + 1] = ll;
       __syncthreads();
-      if (way == 0) {
-#pragma unroll
-        for (int k = 1; k < kWays; ++k) {
-          const float mk = part[warp + k][D], mn = fmaxf(mm, mk), base = mn == -INFINITY ? 0.0f : mn;
-          const float a = ex2(mm - base), w = ex2(mk - base);
+      if (mine && way == 0)
+        for (int q = 1; q < ways; ++q) {
+          const float mk = part[warp + q][D], mn = fmaxf(mm, mk), base = mn == -INFINITY ? 0.0f : mn;
+          const float a = ex2(mm - base), e_q = ex2(mk - base);
           mm = mn;
-          ll = ll * a + w * part[warp + k][D + 1];
+          ll = ll * a + e_q * part[warp + q][D + 1];
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) sum[e] = sum[e] * a + w * part[warp + k][lane * kCols + e];
+          for (int e = 0; e < kCols; ++e) sum[e] = sum[e] * a + e_q * part[warp + q][lane * kCols + e];
         }
-      }
     }
-    if (r < pairs && way == 0) {
-      const size_t at = row_of(p, s, hk, pair0 + r);
+    if (mine && way == 0) {
+      const size_t at = row_of(p, w, r);
       const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
       uint32_t* out = reinterpret_cast<uint32_t*>(p.o + at * D) + lane * (kCols / 2);
 #pragma unroll
