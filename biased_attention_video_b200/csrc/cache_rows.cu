@@ -149,11 +149,15 @@ __device__ __forceinline__ long long scan_warp(long long v) {  // inclusive
 template <int R, int NT>
 struct Line {
   long long total, lo, mine;  // lo, mine: of sequence threadIdx.x, for B <= NT
+  Seq seq;                    // that sequence
   __device__ __forceinline__ explicit Line(const CacheAttnParams& p) {
     __shared__ long long sums[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     mine = 0;
-    for (int b = tid; b < p.b.B; b += NT) mine += load_seq<R>(p, b).units;
+    for (int b = tid; b < p.b.B; b += NT) {
+      seq = load_seq<R>(p, b);
+      mine += seq.units;
+    }
     const long long incl = scan_warp(mine);
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
@@ -165,20 +169,24 @@ struct Line {
       total += sums[w];
     }
   }
-  // The sequence that unit u lies in, and the line before that sequence.
-  __device__ __forceinline__ int find(const CacheAttnParams& p, long long u, long long* before) const {
+  // The sequence that unit u lies in, its number, and the line before it.
+  __device__ __forceinline__ int find(const CacheAttnParams& p, long long u, long long* before, Seq* s) const {
     __shared__ long long sums[NT / 32], at;
     __shared__ int found;
+    __shared__ Seq found_seq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.b.B <= NT) {
       if (u >= lo && u < lo + mine) {
         found = tid;
+        found_seq = seq;
         at = lo;
       }
     } else {
       long long base = 0;
       for (int b0 = 0; b0 < p.b.B && base <= u; b0 += NT) {
-        const long long units = b0 + tid < p.b.B ? load_seq<R>(p, b0 + tid).units : 0;
+        Seq mine_now{};
+        if (b0 + tid < p.b.B) mine_now = load_seq<R>(p, b0 + tid);
+        const long long units = mine_now.units;
         const long long incl = scan_warp(units);
         __syncthreads();
         if (lane == 31) sums[warp] = incl;
@@ -191,12 +199,14 @@ struct Line {
         }
         if (u >= from && u < from + units) {
           found = b0 + tid;
+          found_seq = mine_now;
           at = from;
         }
       }
     }
     __syncthreads();
     *before = at;
+    *s = found_seq;
     return found;
   }
 };
@@ -294,14 +304,16 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
   const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(smem + L::kQ);
   float2* ml = reinterpret_cast<float2*>(smem + L::kMl);  // [warp][R] (maximum, sum)
 
+  wait_dependency();
   launch_dependents();
   const Line<R, kThreads> line(p);
   const long long total = line.total, share = share_of(total);
   const long long u0 = blockIdx.x * share, u1 = min(total, u0 + share);
   if (u0 >= u1) return;
   long long before;
-  const int b0 = line.find(p, u0, &before);
-  Piece1 w = piece_at<R>(p, b0, load_seq<R>(p, b0), before, u0, u1);
+  Seq s0;
+  const int b0 = line.find(p, u0, &before, &s0);
+  Piece1 w = piece_at<R>(p, b0, s0, before, u0, u1);
   if (w.page0 >= w.page1) {  // the rest of an item of one page, which the block before has
     if (w.end >= u1) return;
     w = piece_after<R>(p, w, w.end, u1);
@@ -640,8 +652,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const CacheAttnPa
     return;
   }
   long long before;
-  const int b = line.find(p, u, &before);
-  const Piece1 w = piece_at<R>(p, b, load_seq<R>(p, b), before, u, total);
+  Seq s;
+  const int b = line.find(p, u, &before, &s);
+  const Piece1 w = piece_at<R>(p, b, s, before, u, total);
   wait_dependency();
   if (w.start == u || w.s.pages == 1) return;  // the border lies between two items, or one block has all of it
   const long long c0 = w.start / share;
@@ -714,8 +727,7 @@ cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
   auto kernel = p.q_times != nullptr ? rows_kernel<D, NT, true> : rows_kernel<D, NT, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<kGrid, kThreads, bytes, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_after(kernel, dim3(kGrid), kThreads, bytes, stream, p)) != cudaSuccess) return e;
   return launch_after(join_kernel<D, NT>, dim3(kGrid - 1), 32 * kJoinWarps, 0, stream, p);
 }
 
