@@ -10,6 +10,7 @@ float32 [S]; kv_sel int32 [H, n_video_blocks, k].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
@@ -376,11 +377,18 @@ def tail_correct(p: Plan, v, kv_sel, o, lse, ws, tail_ws=None, stream=None) -> N
 # ------------------------------------------------------------- paged int8 cache
 
 
-def _want(t, name: str, dtype, shape, device):
-    """A contiguous tensor of this type, shape (None: any extent) and device, or an error that says which."""
-    if not (t.dtype == dtype and t.device == device and t.is_contiguous() and t.dim() == len(shape)
-            and all(w is None or w == n for w, n in zip(shape, t.shape))):
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}, not "
+def _is(t, dtype, shape, dev: int) -> bool:
+    """Contiguous, of this type, shape and device index (the checks of every call, cheapest form)."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _name(dev: int) -> str:
+    return f"cuda:{dev}" if dev >= 0 else "cpu"
+
+
+def _want(t, name: str, dtype, shape, dev: int):
+    if not _is(t, dtype, shape, dev):
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {_name(dev)}, not "
                          f"{t.dtype} {list(t.shape)} on {t.device}")
     return t
 
@@ -395,11 +403,12 @@ class Cache:
         if not (k.is_cuda and k.dtype == torch.int8 and k.dim() == 4 and k.shape[2] == 64 and k.is_contiguous()):
             raise ValueError("k must be contiguous CUDA int8 [n_pages, H, 64, d]")
         n, H, _, d = k.shape
-        _want(v, "v", torch.int8, k.shape, k.device)
-        _want(k_scale, "k_scale", torch.float32, (n, H), k.device)
-        _want(v_scale, "v_scale", torch.float32, (n, H), k.device)
+        dev = k.get_device()
+        _want(v, "v", torch.int8, k.shape, dev)
+        _want(k_scale, "k_scale", torch.float32, (n, H), dev)
+        _want(v_scale, "v_scale", torch.float32, (n, H), dev)
         if times is not None:
-            _want(times, "times", torch.float32, (n, 64), k.device)
+            _want(times, "times", torch.float32, (n, 64), dev)
         self._t = (k, v, k_scale, v_scale, times)
         self._c = _CacheStruct(n, H, d, 64, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                _dptr(times))
@@ -429,10 +438,11 @@ class Rope:
     __slots__ = ("_t", "_c")
 
     def __init__(self, cos, sin, index=None, interleaved: bool = False):
-        _want(cos, "cos", torch.float32, (None, None), cos.device)
-        _want(sin, "sin", torch.float32, cos.shape, cos.device)
+        if not (cos.dtype == torch.float32 and cos.dim() == 2 and cos.is_contiguous()):
+            raise ValueError("cos must be contiguous float32 [n_pos, dim / 2]")
+        _want(sin, "sin", torch.float32, cos.shape, cos.get_device())
         if index is not None:
-            _want(index, "index", torch.int32, (None,), cos.device)
+            _want(index, "index", torch.int32, (index.numel(),), cos.get_device())
         self._t = (cos, sin, index)
         self._c = _RopeStruct(cos.data_ptr(), sin.data_ptr(), _dptr(index), cos.shape[0], 2 * cos.shape[1],
                               int(interleaved))
@@ -446,94 +456,90 @@ def cache_workspace(c: Cache, H: int, T: int, B: int) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=c.device)
 
 
-def _batch(c: Cache, T: int, row_start, length, page_table) -> _BatchStruct:
-    dev, i32 = c._t[0].device, torch.int32
-    _want(page_table, "page_table", i32, (None, None), dev)
+def _batch(dev: int, T: int, row_start, length, page_table) -> _BatchStruct:
+    i32 = torch.int32
+    if not (page_table.dim() == 2 and _is(page_table, i32, page_table.shape, dev)):
+        raise ValueError(f"page_table must be contiguous int32 [B, max_pages] on cuda:{dev}")
     B, width = page_table.shape
     _want(row_start, "row_start", i32, (B + 1,), dev)
     _want(length, "length", i32, (B,), dev)
     return _BatchStruct(B, T, width, row_start.data_ptr(), length.data_ptr(), page_table.data_ptr())
 
 
-def _rows(t, name: str, H, d: int, device):
-    """A bf16 [H, T, d] tensor of any head and row stride (rows themselves contiguous)."""
-    if not (t.dtype == torch.bfloat16 and t.device == device and t.dim() == 3 and t.shape[2] == d
-            and (H is None or t.shape[0] == H) and (t.stride(2) == 1 or t.numel() == 0)):
-        raise ValueError(f"{name} must be bf16 [{'H' if H is None else H}, T, {d}] on {device} with contiguous rows")
-    return t
+def _rows(t, name: str, H, d: int, dev: int):
+    """A bf16 [H, T, d] tensor of any head and row stride (rows themselves contiguous): T, head stride, row stride.
+    The stride of an extent of one does not matter and may be anything."""
+    shape = t.shape
+    if not (t.dtype is torch.bfloat16 and len(shape) == 3 and shape[2] == d and (H is None or shape[0] == H)
+            and t.get_device() == dev):
+        raise ValueError(f"{name} must be bf16 [{'H' if H is None else H}, T, {d}] on cuda:{dev}")
+    h, r, x = t.stride()
+    if x != 1 and t.numel() != 0:
+        raise ValueError(f"{name} must have contiguous rows")
+    return shape[1], h if shape[0] > 1 else 0, r if shape[1] > 1 else 0
 
 
-def _strides(t):
-    """Head and row stride; that of an extent of one row or head does not matter and may be anything."""
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+def _on(dev: int, stream):
+    """Context in which the cache's device and the call's stream are current."""
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return _HERE
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
 
 
-class _on:
-    """The device and stream of a cache call: the cache's device is current inside, and so is the stream."""
-
-    __slots__ = ("stream", "_ctx")
-
-    def __init__(self, device, stream):
-        self._ctx = []
-        if device.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            self._ctx.append(torch.cuda.stream(stream))
-        self.stream = stream
-
-    def __enter__(self):
-        for x in self._ctx:
-            x.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *a):
-        for x in reversed(self._ctx):
-            x.__exit__(*a)
+_HERE = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle without building a Stream object
 
 
 def cache_append(c: Cache, k, v, row_start, length, page_table, rope: Optional[Rope] = None, row_times=None, ws=None,
                  stream=None) -> None:
     """Append rows to the cache (h3attn_cache_append): k, v bf16 [H, T, d] (any head and row strides that are multiples
     of 8), packed row row_start[b] + i becomes row length[b] + i of sequence b; keys rotated by ``rope``."""
-    dev = c._t[0].device
-    H, T, d = c._c.H, k.shape[1] if k.dim() == 3 else -1, c._c.d
-    _rows(k, "k", H, d, dev)
-    if _rows(v, "v", H, d, dev).shape[1] != T:
+    cs = c._c
+    dev = c._t[0].get_device()
+    T, kh, kr = _rows(k, "k", cs.H, cs.d, dev)
+    Tv, vh, vr = _rows(v, "v", cs.H, cs.d, dev)
+    if Tv != T:
         raise ValueError("k and v must have the same rows")
-    b = _batch(c, T, row_start, length, page_table)
-    if rope is not None and (rope._t[0].device != dev or (rope._t[2] is not None and rope._t[2].shape[0] != T)):
+    b = _batch(dev, T, row_start, length, page_table)
+    if rope is not None and (rope._t[0].get_device() != dev or (rope._t[2] is not None and rope._t[2].shape[0] != T)):
         raise ValueError("rope must be on the cache's device, its index of T entries")
     if row_times is not None:
         _want(row_times, "row_times", torch.float32, (T,), dev)
-    with _on(dev, stream) as st:
+    with _on(dev, stream):
         if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
-        _raise(lib().h3attn_cache_append(c._c, b, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v),
-                                         rope._c if rope is not None else None, _dptr(row_times),
-                                         ws.data_ptr(), ws.numel(), st), "cache_append")
+            ws = torch.zeros(256, dtype=torch.uint8, device=c.device)
+        rc = lib().h3attn_cache_append(cs, b, k.data_ptr(), kh, kr, v.data_ptr(), vh, vr,
+                                       rope._c if rope is not None else None, _dptr(row_times), ws.data_ptr(),
+                                       ws.numel(), _raw_stream(dev))
+    _raise(rc, "cache_append")
 
 
 def cache_read(c: Cache, row_start, first, page_table, T: Optional[int] = None, k_out=None, v_out=None, ws=None,
                stream=None):
     """Cached rows as bf16 [H, T, d] (h3attn_cache_read): packed row row_start[b] + i gets row first[b] + i of sequence
     b.  T packed rows, or the buffers k_out and v_out (both, or one for K or V alone); returns (k, v)."""
-    dev = c._t[0].device
-    H, d = c._c.H, c._c.d
-    with _on(dev, stream) as st:
+    cs = c._c
+    dev = c._t[0].get_device()
+    with _on(dev, stream):
         if k_out is None and v_out is None:
             if T is None:
                 raise ValueError("cache_read needs T or an output buffer")
-            k_out = torch.empty((H, T, d), dtype=torch.bfloat16, device=dev)
+            k_out = torch.empty((cs.H, T, cs.d), dtype=torch.bfloat16, device=c.device)
             v_out = torch.empty_like(k_out)
         rows = T if T is not None else (k_out if k_out is not None else v_out).shape[1]
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is not None:
-                _want(t, name, torch.bfloat16, (H, rows, d), dev)
-        b = _batch(c, rows, row_start, first, page_table)
+        if k_out is not None:
+            _want(k_out, "k_out", torch.bfloat16, (cs.H, rows, cs.d), dev)
+        if v_out is not None:
+            _want(v_out, "v_out", torch.bfloat16, (cs.H, rows, cs.d), dev)
+        b = _batch(dev, rows, row_start, first, page_table)
         if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
-        _raise(lib().h3attn_cache_read(c._c, b, _dptr(k_out), _dptr(v_out), ws.data_ptr(), ws.numel(), st),
-               "cache_read")
+            ws = torch.zeros(256, dtype=torch.uint8, device=c.device)
+        rc = lib().h3attn_cache_read(cs, b, _dptr(k_out), _dptr(v_out), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    _raise(rc, "cache_read")
     return k_out, v_out
 
 
@@ -543,26 +549,27 @@ def cache_forward(c: Cache, q, row_start, length, page_table, causal: bool = Fal
     """Attention of packed query rows q bf16 [H, T, d] over the cached rows [0, length[b]) of their sequence
     (h3attn_cache_forward); (o, lse) is one partition for merge().  The penalty needs q_times (float32 [T], NaN for
     rows without one) and the cache's times.  Rows of a new ``out`` that belong to no sequence are not written."""
-    dev = c._t[0].device
-    _rows(q, "q", None, c._c.d, dev)
-    H, T, d = q.shape
-    b = _batch(c, T, row_start, length, page_table)
+    cs = c._c
+    dev = c._t[0].get_device()
+    T, qh, qr = _rows(q, "q", None, cs.d, dev)
+    H, d = q.shape[0], cs.d
+    b = _batch(dev, T, row_start, length, page_table)
     pn = _pen(pen)
     if q_times is not None:
         _want(q_times, "q_times", torch.float32, (T,), dev)
     if out is not None:
         _want(out, "out", torch.bfloat16, (H, T, d), dev)
-    if isinstance(lse, torch.Tensor):
+    given = isinstance(lse, torch.Tensor)
+    if given:
         _want(lse, "lse", torch.float32, (H, T), dev)
-    with _on(dev, stream) as st:
-        o = torch.empty((H, T, d), dtype=torch.bfloat16, device=dev) if out is None else out
-        lse_t = lse if isinstance(lse, torch.Tensor) else (
-            torch.empty((H, T), dtype=torch.float32, device=dev) if lse else None)
+    with _on(dev, stream):
+        o = torch.empty((H, T, d), dtype=torch.bfloat16, device=c.device) if out is None else out
+        lse_t = lse if given else torch.empty((H, T), dtype=torch.float32, device=c.device) if lse else None
         if ws is None:
             ws = cache_workspace(c, H, T, b.B)
-        _raise(lib().h3attn_cache_forward(c._c, b, H, max_rows or 0, q.data_ptr(), *_strides(q),
-                                          int(causal), pn, _dptr(q_times), o.data_ptr(), _dptr(lse_t), ws.data_ptr(),
-                                          ws.numel(), st), "cache_forward")
+        rc = lib().h3attn_cache_forward(cs, b, H, max_rows or 0, q.data_ptr(), qh, qr, int(causal), pn, _dptr(q_times),
+                                        o.data_ptr(), _dptr(lse_t), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    _raise(rc, "cache_forward")
     return o, lse_t
 
 

@@ -375,6 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           return alpha;
         };
 
+        auto top32 = [&](const float (&s)[32]) -> float {
+          float mp[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mp[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+          for (int i = 8; i < 32; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mp[e] = max3f(mp[e], s[i + e], s[i + 4 + e]);
+          return fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]);
+        };
+
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t q = done + j;
           const int slot = q & 3;
@@ -396,16 +407,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
             auto load32 = [&](float (&to)[32], int col) {
               __syncwarp();
               tmem_ld32f(t_s + col, to);
-            };
-            auto top32 = [&](const float (&s)[32]) -> float {
-              float mp[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mp[i] = fmaxf(s[i], s[i + 4]);
-#pragma unroll
-              for (int i = 8; i < 32; i += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mp[e] = max3f(mp[e], s[i + e], s[i + 4 + e]);
-              return fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]);
             };
             auto probs32 = [&](const float (&s)[32], float off, float c, uint32_t* to) -> float {
               return probs16_fast(s, off, c, to) + probs16_fast(s + 16, off, c, to + 8);
@@ -455,43 +456,45 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
               warm = __all_sync(kFull, m > -INFINITY);
             }
           } else {
-            // Validity, visibility and penalty key by key, in two passes.  Keys from
-            // `end` on (within the 32 of a load) are not seen; branch-free, as every
-            // lane has an end of its own.
+            // Validity, visibility and penalty key by key, 32 keys at a time.  Keys from
+            // `end` on are not seen; branch-free, as every lane has an end of its own.
             auto scores32 = [&](float (&s)[32], int c, auto timed) {
               const PageMeta& pg = c < 2 ? pa : pb;
               const float pen = c < 2 ? pen_a : pen_b;
               const int end = min(pg.live - (c & 1) * 32, lim - key0 - c * 32);
-              __syncwarp();
-              tmem_ld32f(t_s + c * 32, s);
-              tmem_landed(s);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float q = decltype(timed)::value ? block_penalty_log2(tq, times[c * 32 + i], p) : pen;
                 s[i] = i < end ? fmaf(s[i], pg.c, -q) : -INFINITY;
               }
             };
-            auto any_scores32 = [&](float (&s)[32], int c) {
-              if (kPen && (c < 2 ? pa.mode : pb.mode) == 2) scores32(s, c, std::true_type{});
-              else scores32(s, c, std::false_type{});
-            };
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float s[32];
-              any_scores32(s, c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, s[i]);
-            }
-            raise(mx);
-            warm = __all_sync(kFull, m > -INFINITY);
-            const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const float vs = c < 2 ? pa.vs : pb.vs;
               float s[32];
               uint32_t pk[16];
-              any_scores32(s, c);
+              __syncwarp();
+              tmem_ld32f(t_s + c * 32, s);
+              tmem_landed(s);
+              if (kPen && (c < 2 ? pa.mode : pb.mode) == 2) scores32(s, c, std::true_type{});
+              else scores32(s, c, std::false_type{});
+              const float top = top32(s);
+              if (__any_sync(kFull, top > m + kRescaleThreshold)) {  // what is stored of this step follows the new maximum
+                const float alpha = raise(top);
+#pragma unroll 1
+                for (int k = 0; k < c; ++k) {
+                  uint32_t w[16];
+                  __syncwarp();
+                  tmem_ld16(t_s + k * 16, w);
+                  tmem_landed(w);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    w[i] = pack_bf16(__uint_as_float(w[i] << 16) * alpha, __uint_as_float(w[i] & 0xFFFF0000u) * alpha);
+                  __syncwarp();
+                  tmem_st16(t_s + k * 16, w);
+                }
+              }
+              const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 const float e0 = ex2(s[i] - base), e1 = ex2(s[i + 1] - base);
@@ -502,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
               __syncwarp();
               tmem_st16(t_s + c * 16, pk);
             }
+            warm = __all_sync(kFull, m > -INFINITY);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -668,8 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t q = done + j, buf = q & 1u, ph = (q >> 1) & 1u, next = (q + 1) & 1u;
         for (int sub = 0; ok && sub < subs; ++sub) {
-          ok = wait_bar(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
-          if (ok && sub == 0) ok = wait_bar(v_full + buf, ph, p, abort_flag);
+          if (sub == 0) {
+            ok = wait_bar(v_full + buf, ph, p, abort_flag);
+            if (ok && j + 1 < n) ok = wait_bar(k_full + next, ((q + 1) >> 1) & 1u, p, abort_flag);
+          }
+          ok = ok && wait_bar(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -678,9 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
                     v_d + ((buf * L::kBlockBytes + kk * 2048) >> 4), kIdescO, j > 0 || kk > 0 ? 1u : 0u);
           if (sub == subs - 1) umma_commit(v_empty + buf);
           if (j + 1 < n) {
-            if (sub == 0) ok = wait_bar(k_full + next, ((q + 1) >> 1) & 1u, p, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
             issue_s(sub, next);
             if (sub == subs - 1) umma_commit(k_empty + next);
           }
