@@ -14,7 +14,7 @@
 //                     they also bring Q in and the output out
 //   warps 8..11       keys and values: 16-byte loads of codes, held one step ahead
 //                     in registers, widened and stored as bf16 in the swizzled
-//                     layout the products read (two buffers of K and of V)
+//                     layout the products read (one buffer of K, two of V)
 //   warp 12           TMEM owner and single-thread tcgen05.mma issuer (13..15 idle)
 //
 // TMEM (512 columns): S_A [0, 128), S_B [128, 256), O_A from 256, O_B from 256 + d.
@@ -24,12 +24,18 @@
 // before PV_A(j) has read it, and when S_A(j+1) is complete so is PV_A(j), so a
 // rescale of O_A needs no wait of its own.
 //
+// The issuing thread is on the critical path and every barrier it touches costs it
+// 150 to 200 cycles (a commit right behind another one 500 to 1000), so it waits
+// three times a step (the next keys, the probabilities of A and of B) and commits
+// twice (the scores of A and of B); all else follows from the order: the scores of
+// step j being complete, its keys and the values of step j - 1 are free again.
+//
 // The columns of K, V and Q are stored with every group of four in the order
 // (0, 2, 1, 3), as the codes widen; the products do not see it, and O comes back
 // in the same order.
 //
-// Work split: an item is one tile of one sequence and K/V head, its units are the
-// steps up to the last key that any of its rows sees.  All items form one line,
+// Work split: an item is one tile of one sequence and K/V head, its steps go up to
+// the last key that any of its rows sees.  All items form one line,
 // sequence by sequence, head by head, tile by tile; the blocks share it evenly,
 // and an item that lies in several blocks is joined by another launch from
 // partial results (maximum, sum, unnormalised O in fp32).  The line is laid out
@@ -51,7 +57,10 @@ constexpr int kWidenWarp = 8;
 constexpr int kTile = 256;   // pairs of an item
 constexpr int kStep = 128;   // keys of a step
 constexpr int kGrid = 148;   // one block per SM
-constexpr long long kMinShare = 2;
+// What beginning and ending an item costs (Q, the wait for the first step, the
+// output), in steps: it counts in the line.
+constexpr int kItemCost = 4;
+constexpr long long kMinShare = kItemCost + 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;
 
@@ -79,6 +88,9 @@ __device__ __forceinline__ int tile_steps(const CacheAttnParams& p, const Seq& s
   return max(1, (seen + kStep - 1) / kStep);
 }
 
+// The step that unit x of an item begins (0 <= x <= kItemCost + steps).
+__device__ __forceinline__ int step_at(int x, int steps) { return min(steps, max(0, x - kItemCost)); }
+
 // base[b]: the line before sequence b; base[B]: its length.  One block, one warp
 // per sequence at a time.
 __global__ void __launch_bounds__(1024) plan_kernel(const CacheAttnParams p) {
@@ -96,11 +108,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const CacheAttnParams p) {
     if (b < p.b.B) {
       const Seq s = load_seq(p, b);
       if (p.causal) {
-        for (int t = lane; t < s.tiles; t += 32) u += tile_steps(p, s, t);
+        for (int t = lane; t < s.tiles; t += 32) u += kItemCost + tile_steps(p, s, t);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
       } else {
-        u = (long long)s.tiles * tile_steps(p, s, 0);
+        u = (long long)s.tiles * (kItemCost + tile_steps(p, s, 0));
       }
     }
     if (lane == 0) units[warp] = u * p.c.H;
@@ -128,6 +140,10 @@ struct Item {
   int pairs;         // of the tile
   int steps;         // of the whole item
   long long start;   // the line before the item
+  __device__ __forceinline__ int units() const { return kItemCost + steps; }
+  __device__ __forceinline__ int step(long long u) const {
+    return step_at((int)max(0ll, min((long long)units(), u - start)), steps);
+  }
 };
 __device__ __forceinline__ Item find_item(const CacheAttnParams& p, long long u) {
   const int lane = threadIdx.x & 31;
@@ -151,14 +167,13 @@ __device__ __forceinline__ Item find_item(const CacheAttnParams& p, long long u)
   int t = 0;
   if (!p.causal) {
     it.steps = tile_steps(p, s, 0);
-    t = (int)((u - head_lo) / it.steps);
-    it.start = head_lo + (long long)t * it.steps;
+    t = (int)((u - head_lo) / it.units());
+    it.start = head_lo + (long long)t * it.units();
   } else {
     long long at = head_lo;
-    it.steps = 1;
     it.start = head_lo;
     for (int t0 = 0; t0 < s.tiles; t0 += 32) {
-      const int mine = t0 + lane < s.tiles ? tile_steps(p, s, t0 + lane) : 0;
+      const int mine = t0 + lane < s.tiles ? kItemCost + tile_steps(p, s, t0 + lane) : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -169,12 +184,12 @@ __device__ __forceinline__ Item find_item(const CacheAttnParams& p, long long u)
       if (past != 0u) {
         const int l = __ffs(past) - 1;
         t = t0 + l;
-        it.steps = __shfl_sync(kFull, mine, l);
-        it.start = at + __shfl_sync(kFull, incl, l) - it.steps;
+        it.start = at + __shfl_sync(kFull, incl - mine, l);
         break;
       }
       at += __shfl_sync(kFull, incl, 31);
     }
+    it.steps = tile_steps(p, s, t);
   }
   it.pair0 = (long long)t * kTile;
   it.pairs = (int)min((long long)kTile, (long long)s.n * p.group - it.pair0);
@@ -219,13 +234,13 @@ struct TilesLayout {
   static constexpr int kAtom = 128 * 128;      // one 128-byte-wide column of 128 rows
   static constexpr int kBlockBytes = kHalves * kAtom;  // a Q tile, a K or V block
   static constexpr int kQ = 0;                 // tiles A, B
-  static constexpr int kK = 2 * kBlockBytes;   // two buffers
-  static constexpr int kV = 4 * kBlockBytes;   // two buffers
+  static constexpr int kK = 2 * kBlockBytes;
+  static constexpr int kV = 3 * kBlockBytes;   // two buffers
   static constexpr int kMetaSlots = 4;
-  static constexpr int kMeta = 6 * kBlockBytes;                // [4] x 2 pages
+  static constexpr int kMeta = 5 * kBlockBytes;                // [4] x 2 pages
   static constexpr int kTimes = kMeta + kMetaSlots * 2 * (int)sizeof(PageMeta);  // [4][128]
   static constexpr int kBars = kTimes + kMetaSlots * kStep * 4;
-  static constexpr int kNumBars = 2 + 2 + 2 + 2 + 4 + 1 + 2 + 2 + 1 + 1;
+  static constexpr int kNumBars = 1 + 1 + 4 + 1 + 2 + 2 + 1 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM base, abort flag
   static constexpr int kItem = kMisc + 16;
   static constexpr int kBytes = 1024 + kItem + (int)sizeof(Item) + 16;
@@ -240,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint64_t *k_full = bar, *k_empty = bar + 2, *v_full = bar + 4, *v_empty = bar + 6, *m_full = bar + 8,
-           *q_full = bar + 12, *s_full = bar + 13, *p_full = bar + 15, *o_final = bar + 17, *drain = bar + 18;
+  uint64_t *k_full = bar, *v_full = bar + 1, *m_full = bar + 2, *q_full = bar + 6, *s_full = bar + 7,
+           *p_full = bar + 9, *o_final = bar + 11, *drain = bar + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   Item* item_slot = reinterpret_cast<Item*>(smem + L::kItem);
@@ -258,14 +273,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   if (*abort_flag) return;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 4);
-      mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, 4);
-      mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
     }
     for (int i = 0; i < L::kMetaSlots; ++i) mbar_init(m_full + i, 4);
+    mbar_init(k_full, 4);
+    mbar_init(v_full, 4);
     mbar_init(q_full, 8);
     mbar_init(o_final, 1);
     mbar_init(drain, 1);
@@ -285,32 +298,38 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   // after a give-up.
   long long u = u0;
   Item it;
-  int step0 = 0, n = 0, subs = 0;
-  uint32_t items = 0;               // items before
-  uint32_t done = 0, done_b = 0;    // their steps, and the steps of those with a tile B
+  int step0 = 0, n = 0;
+  int subs = 0;  // tiles that have rows
+  bool began = false;  // began: the item's first unit is this block's
+  uint32_t items = 0;                        // items before
+  uint32_t done = 0, done_b = 0;             // their steps, and the steps of those with a tile B
   auto next = [&]() -> bool {
     if (n > 0) {
       ++items;
       done += (uint32_t)n;
       if (subs == 2) done_b += (uint32_t)n;
-      u += n;
     }
     // every role is done with the last item's buffers
     __syncwarp();
     tc_fence_before();
     block_sync();
     tc_fence_after();
-    if (u >= u1 || *abort_flag) return false;
-    if (warp == kMmaWarp + 1) {
-      const Item x = find_item(p, u);
-      if (lane == 0) *item_slot = x;
-      __syncwarp();
+    if (*abort_flag) return false;
+    for (n = 0; n == 0; u = it.start + it.units()) {  // a stretch may touch an item without a step of it
+      if (u >= u1) return false;
+      if (warp == kMmaWarp + 1) {
+        const Item x = find_item(p, u);
+        if (lane == 0) *item_slot = x;
+        __syncwarp();
+      }
+      block_sync();
+      it = *item_slot;
+      block_sync();
+      step0 = it.step(u);
+      n = it.step(u1) - step0;
+      subs = it.pairs > 128 ? 2 : 1;
+      began = u == it.start;
     }
-    block_sync();
-    it = *item_slot;
-    step0 = (int)(u - it.start);
-    n = (int)min((long long)it.steps, u1 - it.start) - step0;
-    subs = it.pairs > 128 ? 2 : 1;
     return true;
   };
 
@@ -336,10 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
               make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632),
                          __byte_perm(w.z, w.w, 0x5410), __byte_perm(w.z, w.w, 0x7632));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
       if (sub < subs) {
         const int lim = valid && p.causal ? max(0, min(it.len, it.len - it.n + row + 1)) : it.len;
         const int lim_all = __reduce_min_sync(kFull, lim);
@@ -387,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         };
 
         for (int j = 0; ok && j < n; ++j) {
-          const uint32_t q = done + j;
+          const uint32_t q = done + j, mine = (sub ? done_b : done) + j;  // steps, and steps of this tile
           const int slot = q & 3;
           ok = __all_sync(kFull, wait_bar(m_full + slot, (q >> 2) & 1u, p, abort_flag));
           if (!ok) break;
@@ -398,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           const bool plain = pa.plain && pb.plain && key0 + kStep <= lim_all;
           const float pen_a = kPen && pa.mode == 1 ? block_penalty_log2(tq, pa.t, p) : 0.0f;
           const float pen_b = kPen && pb.mode == 1 ? block_penalty_log2(tq, pb.t, p) : 0.0f;
-          ok = __all_sync(kFull, wait_bar(s_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag));
+          ok = __all_sync(kFull, wait_bar(s_full + sub, mine & 1u, p, abort_flag));
           if (!ok) break;
           tc_fence_after();
           if (plain) {
@@ -519,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           const bool whole = n == it.steps;
           const size_t at = (size_t)head * p.b.T + it.first + row;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          float* slot = whole ? nullptr : slot_of<D>(p, blockIdx.x, step0 > 0 ? 0 : 1);
+          float* slot = whole ? nullptr : slot_of<D>(p, blockIdx.x, began ? 1 : 0);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float x[32];
@@ -552,10 +571,22 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       const int rlo = lane >> 2, ch = lane & 3;
       // load i: row 32 w + 8 (i / halves) + rlo, 16 codes at 64 (i % halves) + 16 ch
       uint4 kr[kLoads], vr[kLoads];
-      int page = -1;
-      auto find_page = [&](int j) {  // this warp's page of step j, -1 if it holds no valid key
+      // This warp's page of step j, -1 if it holds no valid key; its entry of the
+      // page table is read a step before it is used.
+      int page = -1, entry = -1;
+      auto read_entry = [&](int j) {
         const int no = (step0 + j) * 2 + page_of;
-        page = j < n && no * kBlock < it.len ? page_id(p.c, p.b, it.b, no, p.status) : -1;
+        entry = -1;
+        if (j < n && no * kBlock < it.len) entry = __ldg(p.b.page_table + (size_t)it.b * p.b.max_pages + no);
+      };
+      auto find_page = [&](int j) {
+        const int no = (step0 + j) * 2 + page_of;
+        page = entry;
+        if (j < n && no * kBlock < it.len && (page < 0 || page >= p.c.n_pages)) {
+          cache_report(p.status, kStatusData);
+          page = -1;
+        }
+        read_entry(j + 1);
       };
       auto load = [&](const int8_t* codes, uint4 (&x)[kLoads]) {
         const int8_t* src = codes + ((size_t)max(page, 0) * p.c.H + it.hk) * kBlock * D;
@@ -591,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           }
         }
       };
+      read_entry(0);
       find_page(0);
       load(p.c.k, kr);
       load(p.c.v, vr);
@@ -598,8 +630,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       for (int j = 0; j < n; ++j) {
         const uint32_t q = done + j;
         const int s = q & 1, slot = q & 3;
-        const uint32_t ph = (q >> 1) & 1u;
-        if (!__all_sync(kFull, wait_bar(k_empty + s, ph ^ 1u, p, abort_flag))) break;
+        // the last step's scores are complete: its keys are read, and the values of the step before it
+        if (j > 0) {
+          const uint32_t last = (subs == 2 ? done_b : done) + j - 1;
+          if (!__all_sync(kFull, wait_bar(s_full + subs - 1, last & 1u, p, abort_flag))) break;
+        }
         // keys of the page that rows may see: 0 for a page past the end or outside the cache
         const int live = page < 0 ? 0 : max(0, min(kBlock, it.len - ((step0 + j) * 2 + page_of) * kBlock));
         if ((w & 1) == 0) {
@@ -627,18 +662,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(m_full + slot);
-        widen(smem + L::kK + s * L::kBlockBytes, kr);
+        widen(smem + L::kK, kr);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + s);
+        if (lane == 0) mbar_arrive(k_full);
         find_page(j + 1);
         load(p.c.k, kr);
         load_meta();
-        if (!__all_sync(kFull, wait_bar(v_empty + s, ph ^ 1u, p, abort_flag))) break;
         widen(smem + L::kV + s * L::kBlockBytes, vr);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + s);
+        if (lane == 0 && j == n - 1) mbar_arrive(v_full);  // else the next step's keys tell
         load(p.c.v, vr);
       }
     }
@@ -653,41 +687,36 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       const uint64_t q_d = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
       const uint64_t k_d = sw128_desc(smem_u32(smem + L::kK), 16, 1024);
       const uint64_t v_d = sw128_desc(smem_u32(smem + L::kV), L::kAtom, 1024);
-      auto issue_s = [&](int sub, uint32_t buf) {
+      auto issue_s = [&](int sub) {
 #pragma unroll
         for (int kk = 0; kk < L::kHalves * 4; ++kk) {
           const uint32_t off = (kk >> 2) * L::kAtom + (kk & 3) * 32;
           umma_ss(tmem + (uint32_t)(128 * sub), q_d + ((sub * L::kBlockBytes + off) >> 4),
-                  k_d + ((buf * L::kBlockBytes + off) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+                  k_d + (off >> 4), kIdescS, kk > 0 ? 1u : 0u);
         }
         umma_commit(s_full + sub);
       };
-      bool ok = wait_bar(q_full, items & 1u, p, abort_flag) &&
-                wait_bar(k_full + (done & 1u), (done >> 1) & 1u, p, abort_flag);
+      auto wait_k = [&](int j) { return wait_bar(k_full, (done + j) & 1u, p, abort_flag); };
+      bool ok = wait_bar(q_full, items & 1u, p, abort_flag) && wait_k(0);
       if (ok) {
         tc_fence_after();
-        for (int sub = 0; sub < subs; ++sub) issue_s(sub, done & 1u);
-        umma_commit(k_empty + (done & 1u));
+        for (int sub = 0; sub < subs; ++sub) issue_s(sub);
       }
       for (int j = 0; ok && j < n; ++j) {
-        const uint32_t q = done + j, buf = q & 1u, ph = (q >> 1) & 1u, next = (q + 1) & 1u;
+        const uint32_t buf = (done + j) & 1u;
+        const bool more = j + 1 < n;
+        // the keys of the next step, and with them this step's values: a widening
+        // warp stores the values of a step before the keys of the next
+        ok = more ? wait_k(j + 1) : wait_bar(v_full, items & 1u, p, abort_flag);
         for (int sub = 0; ok && sub < subs; ++sub) {
-          if (sub == 0) {
-            ok = wait_bar(v_full + buf, ph, p, abort_flag);
-            if (ok && j + 1 < n) ok = wait_bar(k_full + next, ((q + 1) >> 1) & 1u, p, abort_flag);
-          }
-          ok = ok && wait_bar(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
+          ok = wait_bar(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)
             umma_ts(tmem + kTmemO + (uint32_t)(D * sub), tmem + (uint32_t)(128 * sub + 8 * kk),
                     v_d + ((buf * L::kBlockBytes + kk * 2048) >> 4), kIdescO, j > 0 || kk > 0 ? 1u : 0u);
-          if (sub == subs - 1) umma_commit(v_empty + buf);
-          if (j + 1 < n) {
-            issue_s(sub, next);
-            if (sub == subs - 1) umma_commit(k_empty + next);
-          }
+          if (more) issue_s(sub);
         }
       }
       umma_commit(o_final);
@@ -723,7 +752,12 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p
   __syncthreads();
   const Item it = item;
   if (it.start == u || it.start / share != c0) return;
-  const long long c1 = (it.start + it.steps - 1) / share;
+  const long long c1 = (it.start + it.units() - 1) / share;
+  // a block whose stretch touches the item without a step of it has written nothing
+  auto has = [&](long long c) { return it.step((c + 1) * share) > it.step(c * share); };
+  int parts = 0;
+  for (long long c = c0; c <= c1; ++c) parts += has(c) ? 1 : 0;
+  if (parts < 2) return;  // one block has all of it
   const int r0 = blockIdx.y * 32;
   const int i0 = (int)(it.pair0 / p.group), g0 = (int)(it.pair0 % p.group);
   for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
@@ -733,6 +767,7 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (long long c = c0; c <= c1; ++c) {
+      if (!has(c)) continue;
       const float* slot = slot_of<D>(p, c, c == c0 ? 1 : 0);
       const float2 x = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * r);
       const float4 y = *reinterpret_cast<const float4*>(slot + r * D + col);
