@@ -14,7 +14,7 @@
 //                     they also bring Q in and the output out
 //   warps 8..11       keys and values: 16-byte loads of codes, held one step ahead
 //                     in registers, widened and stored as bf16 in the swizzled
-//                     layout the products read (one buffer of K, two of V)
+//                     layout the products read (two buffers of K and of V)
 //   warp 12           TMEM owner and single-thread tcgen05.mma issuer (13..15 idle)
 //
 // TMEM (512 columns): S_A [0, 128), S_B [128, 256), O_A from 256, O_B from 256 + d.
@@ -234,13 +234,13 @@ struct TilesLayout {
   static constexpr int kAtom = 128 * 128;      // one 128-byte-wide column of 128 rows
   static constexpr int kBlockBytes = kHalves * kAtom;  // a Q tile, a K or V block
   static constexpr int kQ = 0;                 // tiles A, B
-  static constexpr int kK = 2 * kBlockBytes;
-  static constexpr int kV = 3 * kBlockBytes;   // two buffers
+  static constexpr int kK = 2 * kBlockBytes;   // two buffers
+  static constexpr int kV = 4 * kBlockBytes;   // two buffers
   static constexpr int kMetaSlots = 4;
-  static constexpr int kMeta = 5 * kBlockBytes;                // [4] x 2 pages
+  static constexpr int kMeta = 6 * kBlockBytes;                // [4] x 2 pages
   static constexpr int kTimes = kMeta + kMetaSlots * 2 * (int)sizeof(PageMeta);  // [4][128]
   static constexpr int kBars = kTimes + kMetaSlots * kStep * 4;
-  static constexpr int kNumBars = 1 + 1 + 4 + 1 + 2 + 2 + 1 + 1;
+  static constexpr int kNumBars = 2 + 1 + 4 + 1 + 2 + 2 + 1 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM base, abort flag
   static constexpr int kItem = kMisc + 16;
   static constexpr int kBytes = 1024 + kItem + (int)sizeof(Item) + 16;
@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint64_t *k_full = bar, *v_full = bar + 1, *m_full = bar + 2, *q_full = bar + 6, *s_full = bar + 7,
-           *p_full = bar + 9, *o_final = bar + 11, *drain = bar + 12;
+  uint64_t *k_full = bar, *v_full = bar + 2, *m_full = bar + 3, *q_full = bar + 7, *s_full = bar + 8,
+           *p_full = bar + 10, *o_final = bar + 12, *drain = bar + 13;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   Item* item_slot = reinterpret_cast<Item*>(smem + L::kItem);
@@ -273,11 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   if (*abort_flag) return;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
     }
     for (int i = 0; i < L::kMetaSlots; ++i) mbar_init(m_full + i, 4);
-    mbar_init(k_full, 4);
     mbar_init(v_full, 4);
     mbar_init(q_full, 8);
     mbar_init(o_final, 1);
@@ -630,19 +630,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       for (int j = 0; j < n; ++j) {
         const uint32_t q = done + j;
         const int s = q & 1, slot = q & 3;
-        // the last step's scores are complete: its keys are read, and the values of the step before it
-        if (j > 0) {
-          const uint32_t last = (subs == 2 ? done_b : done) + j - 1;
-          if (!__all_sync(kFull, wait_bar(s_full + subs - 1, last & 1u, p, abort_flag))) break;
-        }
         // keys of the page that rows may see: 0 for a page past the end or outside the cache
         const int live = page < 0 ? 0 : max(0, min(kBlock, it.len - ((step0 + j) * 2 + page_of) * kBlock));
         if ((w & 1) == 0) {
           PageMeta pm;
           pm.c = ks * p.scale_log2;
           pm.vs = vs;
-          pm.lv = log2f(vs);
-          pm.iv = 1.0f / vs;
+          pm.lv = log2_approx(vs);
+          pm.iv = rcp_approx(vs);
           pm.live = live;
           pm.mode = 0;
           pm.t = 0.0f;
@@ -662,13 +657,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(m_full + slot);
-        widen(smem + L::kK, kr);
+        widen(smem + L::kK + s * L::kBlockBytes, kr);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full);
+        if (lane == 0) mbar_arrive(k_full + s);
         find_page(j + 1);
         load(p.c.k, kr);
         load_meta();
+        // once the last step's scores are complete, the values of the step before it are free, and its own keys
+        if (j > 0) {
+          const uint32_t last = (subs == 2 ? done_b : done) + j - 1;
+          if (!__all_sync(kFull, wait_bar(s_full + subs - 1, last & 1u, p, abort_flag))) break;
+        }
         widen(smem + L::kV + s * L::kBlockBytes, vr);
         fence_proxy_async_smem();
         __syncwarp();
@@ -687,20 +687,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       const uint64_t q_d = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
       const uint64_t k_d = sw128_desc(smem_u32(smem + L::kK), 16, 1024);
       const uint64_t v_d = sw128_desc(smem_u32(smem + L::kV), L::kAtom, 1024);
-      auto issue_s = [&](int sub) {
+      auto issue_s = [&](int sub, uint32_t k_buf) {
 #pragma unroll
         for (int kk = 0; kk < L::kHalves * 4; ++kk) {
           const uint32_t off = (kk >> 2) * L::kAtom + (kk & 3) * 32;
           umma_ss(tmem + (uint32_t)(128 * sub), q_d + ((sub * L::kBlockBytes + off) >> 4),
-                  k_d + (off >> 4), kIdescS, kk > 0 ? 1u : 0u);
+                  k_d + ((k_buf * L::kBlockBytes + off) >> 4), kIdescS, kk > 0 ? 1u : 0u);
         }
         umma_commit(s_full + sub);
       };
-      auto wait_k = [&](int j) { return wait_bar(k_full, (done + j) & 1u, p, abort_flag); };
+      auto wait_k = [&](int j) { return wait_bar(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag); };
       bool ok = wait_bar(q_full, items & 1u, p, abort_flag) && wait_k(0);
       if (ok) {
         tc_fence_after();
-        for (int sub = 0; sub < subs; ++sub) issue_s(sub);
+        for (int sub = 0; sub < subs; ++sub) issue_s(sub, done & 1u);
       }
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t buf = (done + j) & 1u;
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           for (int kk = 0; kk < kStep / 16; ++kk)
             umma_ts(tmem + kTmemO + (uint32_t)(D * sub), tmem + (uint32_t)(128 * sub + 8 * kk),
                     v_d + ((buf * L::kBlockBytes + kk * 2048) >> 4), kIdescO, j > 0 || kk > 0 ? 1u : 0u);
-          if (more) issue_s(sub);
+          if (more) issue_s(sub, buf ^ 1u);
         }
       }
       umma_commit(o_final);
