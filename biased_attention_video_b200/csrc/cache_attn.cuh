@@ -112,6 +112,38 @@ inline cudaError_t launch_after(void (*kernel)(CacheAttnParams), dim3 grid, int 
   return cudaLaunchKernelEx(&c, kernel, p);
 }
 
+// The tcgen05 operations that one thread issues, from a converged warp: one lane
+// (always the same) is elected inside.  Under a branch on the lane the compiler
+// cannot keep the descriptors in uniform registers, and moving them there costs
+// about 50 cycles per product.
+__device__ __forceinline__ void umma_ss_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_one(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // Columns [col, col + 4) of output row `at` (head T + packed row) from unnormalised v; inv = 1 / sum, 0 for no key.
 __device__ __forceinline__ void store_cols(const CacheAttnParams& p, size_t at, int col, float4 v, float inv) {
   *reinterpret_cast<uint2*>(p.o + at * p.c.d + col) =

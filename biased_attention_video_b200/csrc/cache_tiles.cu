@@ -240,11 +240,17 @@ struct TilesLayout {
   static constexpr int kMeta = 6 * kBlockBytes;                // [4] x 2 pages
   static constexpr int kTimes = kMeta + kMetaSlots * 2 * (int)sizeof(PageMeta);  // [4][128]
   static constexpr int kBars = kTimes + kMetaSlots * kStep * 4;
-  static constexpr int kNumBars = 2 + 1 + 4 + 1 + 2 + 2 + 1 + 1;
+  static constexpr int kNumBars = 2 + 1 + 4 + 1 + 4 + 2 + 1 + 1;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM base, abort flag
   static constexpr int kItem = kMisc + 16;
   static constexpr int kBytes = 1024 + kItem + (int)sizeof(Item) + 16;
 };
+
+// wait_bar by a whole warp, with one answer
+template <class Params>
+__device__ __forceinline__ bool wait_bar_all(uint64_t* bar, uint32_t parity, const Params& p, volatile int* abort) {
+  return __all_sync(kFull, wait_bar(bar, parity, p, abort));
+}
 
 // The whole block, from roles that run different code.
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t *k_full = bar, *v_full = bar + 2, *m_full = bar + 3, *q_full = bar + 7, *s_full = bar + 8,
-           *p_full = bar + 10, *o_final = bar + 12, *drain = bar + 13;
+           *p_full = bar + 12, *o_final = bar + 14, *drain = bar + 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   Item* item_slot = reinterpret_cast<Item*>(smem + L::kItem);
@@ -275,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);
       mbar_init(s_full + i, 1);
+      mbar_init(s_full + 2 + i, 1);
       mbar_init(p_full + i, 4);
     }
     for (int i = 0; i < L::kMetaSlots; ++i) mbar_init(m_full + i, 4);
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           const bool plain = pa.plain && pb.plain && key0 + kStep <= lim_all;
           const float pen_a = kPen && pa.mode == 1 ? block_penalty_log2(tq, pa.t, p) : 0.0f;
           const float pen_b = kPen && pb.mode == 1 ? block_penalty_log2(tq, pb.t, p) : 0.0f;
-          ok = __all_sync(kFull, wait_bar(s_full + sub, mine & 1u, p, abort_flag));
+          ok = __all_sync(kFull, wait_bar(s_full + 2 * sub + (mine & 1u), (mine >> 1) & 1u, p, abort_flag));
           if (!ok) break;
           tc_fence_after();
           if (plain) {
@@ -664,10 +671,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         find_page(j + 1);
         load(p.c.k, kr);
         load_meta();
-        // once the last step's scores are complete, the values of the step before it are free, and its own keys
+        // Once the last step's scores are complete, the values of the step before it
+        // are free, and its own keys.  (A tile's steps take two barriers in turn: this
+        // step's scores may be complete as well by now, but not the next one's.)
         if (j > 0) {
           const uint32_t last = (subs == 2 ? done_b : done) + j - 1;
-          if (!__all_sync(kFull, wait_bar(s_full + subs - 1, last & 1u, p, abort_flag))) break;
+          if (!wait_bar_all(s_full + 2 * (subs - 1) + (last & 1u), (last >> 1) & 1u, p, abort_flag)) break;
         }
         widen(smem + L::kV + s * L::kBlockBytes, vr);
         fence_proxy_async_smem();
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     while (next()) {
-      if (warp != kMmaWarp || lane != 0) continue;
+      if (warp != kMmaWarp) continue;
       // ------------------------------------------------------ MMA issuer
       constexpr uint32_t kIdescS = idesc_bf16_f32(128, kStep, 0, 0);
       constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, 0, 1);
@@ -687,44 +696,45 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
       const uint64_t q_d = sw128_desc(smem_u32(smem + L::kQ), 16, 1024);
       const uint64_t k_d = sw128_desc(smem_u32(smem + L::kK), 16, 1024);
       const uint64_t v_d = sw128_desc(smem_u32(smem + L::kV), L::kAtom, 1024);
-      auto issue_s = [&](int sub, uint32_t k_buf) {
+      auto issue_s = [&](int sub, int j) {
+        const uint32_t k_buf = (done + j) & 1u, x = (sub ? done_b : done) + j;
 #pragma unroll
         for (int kk = 0; kk < L::kHalves * 4; ++kk) {
           const uint32_t off = (kk >> 2) * L::kAtom + (kk & 3) * 32;
-          umma_ss(tmem + (uint32_t)(128 * sub), q_d + ((sub * L::kBlockBytes + off) >> 4),
+          umma_ss_one(tmem + (uint32_t)(128 * sub), q_d + ((sub * L::kBlockBytes + off) >> 4),
                   k_d + ((k_buf * L::kBlockBytes + off) >> 4), kIdescS, kk > 0 ? 1u : 0u);
         }
-        umma_commit(s_full + sub);
+        umma_commit_one(s_full + 2 * sub + (x & 1u));
       };
-      auto wait_k = [&](int j) { return wait_bar(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag); };
-      bool ok = wait_bar(q_full, items & 1u, p, abort_flag) && wait_k(0);
+      auto wait_k = [&](int j) { return wait_bar_all(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag); };
+      bool ok = wait_bar_all(q_full, items & 1u, p, abort_flag) && wait_k(0);
       if (ok) {
         tc_fence_after();
-        for (int sub = 0; sub < subs; ++sub) issue_s(sub, done & 1u);
+        for (int sub = 0; sub < subs; ++sub) issue_s(sub, 0);
       }
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t buf = (done + j) & 1u;
         const bool more = j + 1 < n;
         // the keys of the next step, and with them this step's values: a widening
         // warp stores the values of a step before the keys of the next
-        ok = more ? wait_k(j + 1) : wait_bar(v_full, items & 1u, p, abort_flag);
+        ok = more ? wait_k(j + 1) : wait_bar_all(v_full, items & 1u, p, abort_flag);
         for (int sub = 0; ok && sub < subs; ++sub) {
-          ok = wait_bar(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
+          ok = wait_bar_all(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)
-            umma_ts(tmem + kTmemO + (uint32_t)(D * sub), tmem + (uint32_t)(128 * sub + 8 * kk),
+            umma_ts_one(tmem + kTmemO + (uint32_t)(D * sub), tmem + (uint32_t)(128 * sub + 8 * kk),
                     v_d + ((buf * L::kBlockBytes + kk * 2048) >> 4), kIdescO, j > 0 || kk > 0 ? 1u : 0u);
-          if (more) issue_s(sub, buf ^ 1u);
+          if (more) issue_s(sub, j + 1);
         }
       }
-      umma_commit(o_final);
+      umma_commit_one(o_final);
     }
   }
 
-  if (tid == kMmaWarp * 32) {  // all issued MMAs complete before TMEM is released
-    umma_commit(drain);
+  if (warp == kMmaWarp) {  // all issued MMAs complete before TMEM is released
+    umma_commit_one(drain);
     drain_wait(drain, 0, p);
   }
   tc_fence_before();
