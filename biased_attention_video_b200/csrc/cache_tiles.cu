@@ -59,7 +59,7 @@ constexpr int kStep = 128;   // keys of a step
 constexpr int kGrid = 148;   // one block per SM
 // What beginning and ending an item costs (Q, the wait for the first step, the
 // output), in steps: it counts in the line.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 6;
 constexpr long long kMinShare = kItemCost + 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
   Item* item_slot = reinterpret_cast<Item*>(smem + L::kItem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  launch_dependents();
   wait_dependency();
+  launch_dependents();  // after the wait: the join reads the line, too, before it waits for this kernel
   const long long total = p.base[p.b.B], share = share_of(total);
   const long long u0 = blockIdx.x * share, u1 = min(total, u0 + share);
   if (u0 >= u1) return;
@@ -747,50 +747,88 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
 
 // Joins the items that several blocks share: blocks (x, y) look at the border
 // between the stretches x and x + 1 and join the item that lies across it, if it
-// is that item's first border; y takes 32 of its pairs.
+// is that item's first border; y takes 32 of its pairs.  The item, and the slots
+// that hold parts of it, are found by one warp; a thread then takes 4 columns of
+// several pairs, all their loads of a slot issued together.
+constexpr int kJoinThreads = 256, kJoinPairs = 32;
 template <int D>
-__global__ void __launch_bounds__(256) join_tiles_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const CacheAttnParams p) {
+  constexpr int kEach = kJoinPairs * (D / 4) / kJoinThreads;  // pairs of a thread
   __shared__ Item item;
-  wait_dependency();
+  __shared__ int parts, slots[kGrid];
+  const int tid = threadIdx.x, lane = tid & 31;
   const long long total = p.base[p.b.B], share = share_of(total);
-  const long long c0 = blockIdx.x, u = (c0 + 1) * share;
-  if (u >= total) return;
-  if (threadIdx.x < 32) {
+  const int c0 = (int)blockIdx.x;
+  const long long u = (c0 + 1) * share;
+  if (u >= total) {
+    wait_dependency();
+    return;
+  }
+  if (tid < 32) {
     const Item it = find_item(p, u);
-    if (threadIdx.x == 0) item = it;
+    int n = 0;
+    if (it.start < u && it.start >= c0 * share && it.pairs > (int)blockIdx.y * kJoinPairs) {
+      // a block whose stretch touches the item without a step of it has written nothing
+      const long long end = it.start + it.units();
+      for (int c = c0; c * share < end; c += 32) {
+        const long long from = (c + lane) * share;
+        const bool has = from < end && it.step(from + share) > it.step(from);
+        const unsigned who = __ballot_sync(kFull, has);
+        if (has) slots[n + __popc(who & ((1u << lane) - 1u))] = 2 * (c + lane) + (c + lane == c0 ? 1 : 0);
+        n += __popc(who);
+      }
+    }
+    if (lane == 0) {
+      item = it;
+      parts = n;
+    }
   }
   __syncthreads();
+  wait_dependency();
+  const int n = parts;
+  if (n < 2) return;  // not the item's first border, or one block has all of it
   const Item it = item;
-  if (it.start == u || it.start / share != c0) return;
-  const long long c1 = (it.start + it.units() - 1) / share;
-  // a block whose stretch touches the item without a step of it has written nothing
-  auto has = [&](long long c) { return it.step((c + 1) * share) > it.step(c * share); };
-  int parts = 0;
-  for (long long c = c0; c <= c1; ++c) parts += has(c) ? 1 : 0;
-  if (parts < 2) return;  // one block has all of it
-  const int r0 = blockIdx.y * 32;
-  const int i0 = (int)(it.pair0 / p.group), g0 = (int)(it.pair0 % p.group);
-  for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
-    const int r = r0 + i / (D / 4), col = i % (D / 4) * 4;
-    if (r >= it.pairs) break;
-    float mm = -INFINITY, ll = 0.0f;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (long long c = c0; c <= c1; ++c) {
-      if (!has(c)) continue;
-      const float* slot = slot_of<D>(p, c, c == c0 ? 1 : 0);
-      const float2 x = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * r);
-      const float4 y = *reinterpret_cast<const float4*>(slot + r * D + col);
-      const float mn = fmaxf(mm, x.x), base = mn == -INFINITY ? 0.0f : mn;
-      const float a = ex2(mm - base), e = ex2(x.x - base);
-      mm = mn;
-      ll = ll * a + e * x.y;
-      sum.x = sum.x * a + e * y.x, sum.y = sum.y * a + e * y.y;
-      sum.z = sum.z * a + e * y.z, sum.w = sum.w * a + e * y.w;
+  const int col = tid % (D / 4) * 4, r0 = blockIdx.y * kJoinPairs + tid / (D / 4);
+  float mm[kEach], ll[kEach];
+  float4 sum[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    mm[e] = -INFINITY;
+    ll[e] = 0.0f;
+    sum[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  for (int k = 0; k < n; ++k) {
+    const float* slot = p.partial + (size_t)slots[k] * (kTile * (D + 2));
+    float2 x[kEach];
+    float4 y[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int r = r0 + e * (kJoinThreads / (D / 4));
+      if (r < it.pairs) {
+        x[e] = *reinterpret_cast<const float2*>(slot + kTile * D + 2 * r);
+        y[e] = *reinterpret_cast<const float4*>(slot + r * D + col);
+      }
     }
-    const size_t at = (size_t)(it.hk * p.group + (g0 + r) % p.group) * p.b.T + it.first + i0 + (g0 + r) / p.group;
-    store_cols(p, at, col, sum, ll == 0.0f ? 0.0f : 1.0f / ll);
-    if (col == 0) store_lse(p, at, mm, ll);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (r0 + e * (kJoinThreads / (D / 4)) >= it.pairs) continue;
+      const float mn = fmaxf(mm[e], x[e].x), base = mn == -INFINITY ? 0.0f : mn;
+      const float a = ex2(mm[e] - base), w = ex2(x[e].x - base);
+      mm[e] = mn;
+      ll[e] = ll[e] * a + w * x[e].y;
+      sum[e].x = sum[e].x * a + w * y[e].x, sum[e].y = sum[e].y * a + w * y[e].y;
+      sum[e].z = sum[e].z * a + w * y[e].z, sum[e].w = sum[e].w * a + w * y[e].w;
+    }
+  }
+  const int i0 = (int)(it.pair0 / p.group), g0 = (int)(it.pair0 - (long long)i0 * p.group);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int r = r0 + e * (kJoinThreads / (D / 4));
+    if (r >= it.pairs) continue;
+    const int i = (int)((unsigned)(g0 + r) / (unsigned)p.group), g = g0 + r - i * p.group;
+    const size_t at = (size_t)(it.hk * p.group + g) * p.b.T + it.first + i0 + i;
+    store_cols(p, at, col, sum[e], ll[e] == 0.0f ? 0.0f : 1.0f / ll[e]);
+    if (col == 0) store_lse(p, at, mm[e], ll[e]);
   }
 }
 
@@ -803,7 +841,7 @@ cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
   plan_kernel<<<1, 1024, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_after(kernel, dim3(kGrid), kThreads, bytes, stream, p)) != cudaSuccess) return e;
-  return launch_after(join_tiles_kernel<D>, dim3(kGrid - 1, kTile / 32), 256, 0, stream, p);
+  return launch_after(join_tiles_kernel<D>, dim3(kGrid - 1, kTile / kJoinPairs), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace
