@@ -434,7 +434,7 @@ H3ATTN_API int h3attn_check(void* ws, void* stream);
 
 /* Test and diagnostics only: bound every device-side wait of the attention
  * kernels launched by later calls (h3attn_forward, h3attn_dense_biased,
- * h3attn_forward_qk8, h3attn_attend_host) to `polls` unsuccessful polls of its
+ * h3attn_forward_qk8, h3attn_attend_host, h3attn_cache_forward) to `polls` unsuccessful polls of its
  * barrier; 0 restores the default (no poll bound).  The time bound of 2 s per
  * wait always applies, and the waits that drain a give-up (for the kernel's
  * own TMA loads and MMAs already in flight) are bounded by time only, so a

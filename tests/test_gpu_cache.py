@@ -530,3 +530,117 @@ def test_a_marked_page_stays_away_from_rows_that_do_not_see_it(rows):
     assert 0 < clean < rows
     assert torch.equal(o[:, :clean], want[:, :clean]) and torch.equal(l[:, :clean], want_l[:, :clean])
     assert torch.all(torch.isnan(o[:, clean:])) and torch.all(torch.isnan(l[:, clean:]))
+
+
+@pytest.mark.parametrize("rows,H,kv,B,longest", [(2, 4, 2, 500, 300), (1, 2, 2, 193, 700), (40, 2, 1, 70, 260)])
+def test_forward_of_many_sequences(rows, H, kv, B, longest):
+    """More sequences than a block has threads; lengths from nothing on, rows from none on."""
+    rng = np.random.default_rng(B)
+    lengths = [int(x) for x in rng.integers(0, longest, size=B)]
+    n = [int(x) for x in rng.integers(0, rows + 1, size=B)]
+    n[-1] = rows
+    n_pages = sum(-(-x // 64) for x in lengths) + 1
+    c, host = make_cache(n_pages, kv, 64, seed=B)
+    check_forward(c, host, make_table(lengths, n_pages), lengths, n, H, causal=True, seed=B, max_rows=rows)
+
+
+@pytest.mark.parametrize("H,kv,rows", [(300, 1, 3), (40, 1, 1), (33, 1, 9), (64, 2, 1)])
+def test_forward_of_wide_groups(H, kv, rows):
+    """Query heads of one K/V head that fill no whole number of tiles."""
+    lengths = [321, 90]
+    c, host = make_cache(9, kv, 64, seed=H)
+    check_forward(c, host, make_table(lengths, 9), lengths, [rows, 1], H, causal=True, seed=H)
+
+
+def test_forward_of_no_rows():
+    c, _ = make_cache(2, 1, 64)
+    for T in (1, 100):
+        out = torch.full((2, T, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        q = torch.randn(2, T, 64, device=DEV).to(torch.bfloat16)
+        h3.cache_forward(c, q, i32([0, 0, 0]), i32([5, 0]), i32([[0], [1]]), out=out)
+        assert torch.all(out == 7)
+    o, _ = h3.cache_forward(c, q[:, :0], i32([0, 0]), i32([5]), i32([[0]]))
+    assert o.shape == (2, 0, 64)
+
+
+@pytest.mark.parametrize("rows,hint", [(1, 1), (150, 150), (150, 1)])
+def test_forward_repeats_itself(rows, hint):
+    """The same call gives the same bits, also with a hint that is too small."""
+    lengths = [3000, 100, 900]
+    c, host = make_cache(70, 2, 128, seed=15)
+    table = make_table(lengths, 70)
+    first = check_forward(c, host, table, lengths, [rows] * 3, 4, seed=15, max_rows=hint)
+    for _ in range(3):
+        again = check_forward(c, host, table, lengths, [rows] * 3, 4, seed=15, max_rows=hint)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_two_streams_and_two_workspaces():
+    """Calls that overlap, each with a workspace of its own."""
+    lengths = [5000]
+    cs = [make_cache(80, 2, 128, seed=s) for s in (1, 2)]
+    table = make_table(lengths, 80)
+    qs = [torch.randn(8, n, 128, device=DEV).to(torch.bfloat16) for n in (1, 200)]
+    args = [(c, q, i32([0, q.shape[1]]), i32(lengths), i32(table)) for (c, _), q in zip(cs, qs)]
+    want = [h3.cache_forward(*a, lse=True) for a in args]
+    ws = [h3.cache_workspace(a[0], 8, a[1].shape[1], 1) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [h3.cache_forward(*a, ws=w, lse=True, stream=s) for a, w, s in zip(args, ws, streams)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    assert all(h3.check(w) == h3.OK for w in ws)
+
+
+def test_forward_with_short_waits_ends_and_recovers():
+    """Every wait of the tile kernel bounded to one poll.  One poll may itself block for a time that the hardware sets,
+    so a wait may still come through: the call ends either complete or with the status word set; then, with the bound
+    gone and the word cleared, a call on the same workspace is right."""
+    lengths = [2000]
+    c, host = make_cache(40, 2, 128, seed=21)
+    table = make_table(lengths, 40)
+    ws = h3.cache_workspace(c, 2, 300, 1)
+    q = torch.randn(2, 300, 128, device=DEV).to(torch.bfloat16)
+    args = q, i32([0, 300]), i32(lengths), i32(table)
+    want, _ = h3.cache_forward(c, *args)
+    for _ in range(20):
+        try:
+            h3.set_wait_polls(1)
+            o, _ = h3.cache_forward(c, *args, ws=ws)
+            status = h3.check(ws)
+        finally:
+            h3.set_wait_polls(0)
+        assert status in (h3.OK, h3.ETIMEOUT)
+        assert status == h3.ETIMEOUT or torch.equal(o, want)
+        assert h3.check(ws) == h3.OK
+    check_forward(c, host, table, lengths, [300], 2, seed=21, ws=ws)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_forward_of_random_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    d, kv, g = int(rng.choice([64, 128])), int(rng.choice([1, 2, 3])), int(rng.choice([1, 2, 3, 5, 8]))
+    B = int(rng.integers(1, 9))
+    lengths = [int(x) for x in np.exp(rng.uniform(0, np.log(3000), size=B))]
+    rows = [int(x) for x in np.exp(rng.uniform(0, np.log(400), size=B))]
+    n_pages = sum(-(-x // 64) for x in lengths) + 2
+    pen = h3.DEFAULT_PENALTY if seed % 2 else None
+    c, host = make_cache(n_pages, kv, d, seed=seed, times=pen is not None)
+    check_forward(c, host, make_table(lengths, n_pages, seed=seed), lengths, rows, kv * g, causal=bool(seed % 3), pen=pen,
+                  pad=seed, seed=seed, max_rows=max(rows))
+
+
+def test_forward_over_pages_of_one_guide_time():
+    """Pages whose keys share a guide time, pages with two, a page without: the tile kernel's three ways."""
+    lengths, rows = [64 * 6 + 10], [200]
+    c, host = make_cache(7, 1, 128, seed=33, times=True)
+    t = host[4]
+    table = make_table(lengths, 7)
+    for i, p in enumerate(table[0]):
+        t[p] = 0.17 * i
+    t[table[0][2], 20:] = 1.7
+    t[table[0][4]] = float("nan")
+    c.times.copy_(t)
+    check_forward(c, host, table, lengths, rows, 2, pen=h3.DEFAULT_PENALTY, seed=33)
