@@ -72,10 +72,10 @@ struct CacheAttnParams {
   uint64_t wait_ns;
 };
 
-// Row tiles of 8 NT (query row, head of the group) pairs; see cache_rows.cu.
-size_t cache_rows_partial_bytes(int d, long long rows);
-// rows: most (query row, head of the group) pairs of one sequence
-cudaError_t launch_cache_rows(const CacheAttnParams& p, long long rows, cudaStream_t stream);
+// Few rows per sequence; see cache_rows.cu.  pairs: most (query row, head of the
+// group) pairs of one sequence.
+size_t cache_rows_partial_bytes(int d, long long pairs);
+cudaError_t launch_cache_rows(const CacheAttnParams& p, long long pairs, cudaStream_t stream);
 
 // Tensor-core tiles of 256 pairs; see cache_tiles.cu.
 size_t cache_tiles_partial_bytes(int d);

@@ -5,16 +5,16 @@
 //   O = sum_j exp(s_j) code_j s_v / sum_j exp(s_j),   LSE = log sum_j exp(s_j);
 // a row that sees no key gets O = 0 and LSE = -inf.
 //
-// HBM-bound: every code is read once and used for the few rows of one sequence
-// and K/V head.  The query heads of a K/V head and the rows of a sequence form
-// one list of (row, head) pairs, cut into tiles of 8 NT pairs; an item is one
-// tile of one sequence and K/V head, its units are the sequence's pages.  The
-// units of all items form one line that the blocks share evenly, whatever the
-// lengths are (they are read on the device); a block walks its stretch item by
-// item, and items that lie in several blocks are joined by a second launch from
-// partial results (maximum, sum, unnormalised O in fp32).
+// HBM-bound: a code is read once (twice for 17 to 32 pairs, then from L2) and used
+// for the few rows of one sequence and K/V head.  The query heads of a K/V head and
+// the rows of a sequence form one list of (row, head) pairs, cut into tiles of 8 NT
+// pairs; an item is one tile of one sequence and K/V head, its units are the
+// sequence's pages.  The units of all items form one line that the blocks share
+// evenly, whatever the lengths are (they are read on the device); a block walks its
+// stretch item by item, and items that lie in several blocks are joined by a second
+// launch from partial results (maximum, sum, unnormalised O in fp32).
 //
-// Inside a block each warp streams granules of 16 keys on its own: cp.async into
+// Inside a block each warp streams granules of 32 keys on its own: cp.async into
 // a ring of its own (no barrier between warps until the item ends), then
 //   S^T = K Q^T   mma m16n8k16 fp16, A = the codes widened exactly to fp16,
 //   P^T           exp2 of the scaled scores, packed to fp16, transposed by movmatrix,
@@ -28,6 +28,12 @@
 // The d order of A and of Q agree by construction and nothing else sees it, so
 // a lane takes 16 consecutive bytes of a row per load.  mma.sync and not tcgen05:
 // 8 rows fill no 128-row tile, and the widened codes are in registers anyway.
+//
+// Measured: one row of 56 heads over 116,883 rows of 8 K/V heads of 128 (240 MB)
+// 52 us, 32 sequences of 410 to 8,192 rows (282 MB) 59 us: 4.6 and 4.8 TB/s, and
+// about 5.7 TB/s but for the 7 us that two launches and finding the pages take; the
+// same loop without its arithmetic takes 51.5 us and 60 us.  (A plain sum over 240 MB
+// reads 5.3 TB/s.)  In 16-key granules, 8 warps a block: 56 and 73 us.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -49,7 +55,8 @@ constexpr float kShift = 12.0f;  // a probability is 2^kShift at the running max
 constexpr int kBlocksPerSm = 2;
 constexpr int kGrid = 148 * kBlocksPerSm;
 // What beginning and ending an item costs a block, in pages: it counts in the
-// line, so that a block that gets many short sequences gets fewer pages.
+// line, so that a block that gets many short sequences gets fewer pages (the 32
+// ragged sequences: 73 us without, 68 with 1, 60 with 3, 61 with 8).
 constexpr int kItemCost = 3;
 constexpr int kMinShare = kItemCost + 1;
 
@@ -61,12 +68,8 @@ struct RowsLayout {
   static constexpr int kStage = kMeta + 16 + kKeys * 4;
   static constexpr int kPitch = D + 4;              // floats of one row of the warps' results
   static constexpr int kResult = kRows * kPitch * 4;
-  // A warp's results lie behind its ring, so that the next item's first granules
-  // load while the warps' results are joined; over it where that would cost a
-  // block per SM.
-  static constexpr bool kBehind = false;
-  static constexpr int kRes = kBehind ? kStages * kStage : 0;
-  static constexpr int kRing = kBehind ? kRes + kResult : kStages * kStage > kResult ? kStages * kStage : kResult;
+  // a warp's results lie over its ring
+  static constexpr int kRing = kStages * kStage > kResult ? kStages * kStage : kResult;
   static constexpr int kQ = kWarps * kRing;         // Q fragments: [D / 16][NT][32] uint2
   static constexpr int kQScale = kQ + D / 16 * NT * 256;  // [R] powers of two
   static constexpr int kMl = kQScale + kRows * 4;
@@ -294,7 +297,7 @@ __device__ __forceinline__ float* slot_of(const CacheAttnParams& p, long long bl
 // --------------------------------------------------------------- the kernel
 
 template <int D, int NT, bool kPen>
-__global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rows_kernel(const CacheAttnParams p) {
   using L = RowsLayout<D, NT>;
   constexpr int R = L::kRows, kJ = D / 16;
   constexpr bool kQRegs = NT == 1;  // Q fragments in registers, else read from shared memory
@@ -372,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
   load_q();
 
   while (true) {
-    __syncthreads();  // the last item's results and fragments are read
     uint32_t qf[kQRegs ? 2 * kJ : 1];
     if (kQRegs || warp < NT) {
       const int r = (kQRegs ? 0 : warp * 8) + g;
@@ -572,19 +574,15 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
     }
     __syncwarp();  // the ring is read
 
-    // on to the next piece: its first granules and its Q load while this one is joined
+    // on to the next piece: its Q loads while this one is joined
     const Piece1 done = w;
     const long long u = w.end;
     const bool more = u < u1;
     if (more) {
       w = piece_after<R>(p, w, u, u1);
       begin();
-      if constexpr (L::kBehind) {
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(i);
-      }
     }
-    float* res = reinterpret_cast<float*>(ring + L::kRes);
+    float* res = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -612,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
       for (int x = 0; x < kWarps; ++x) {
         const float2 v = ml[x * R + r];
         const float a = v.x == -INFINITY ? 0.0f : ex2(v.x - mm);
-        const float4 y = *reinterpret_cast<const float4*>(smem + x * L::kRing + L::kRes + (r * L::kPitch + col) * 4);
+        const float4 y = *reinterpret_cast<const float4*>(smem + x * L::kRing + (r * L::kPitch + col) * 4);
         ll += a * v.y;
         sum.x += a * y.x, sum.y += a * y.y, sum.z += a * y.z, sum.w += a * y.w;
       }
@@ -626,11 +624,9 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : kBlocksPerSm) rows_kern
       }
     }
     if (!more) break;
-    if constexpr (!L::kBehind) {
-      __syncthreads();
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(i);
-    }
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
   }
   cp_async_wait<0>();
 }
@@ -731,20 +727,21 @@ cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
   return launch_after(join_kernel<D, NT>, dim3(kGrid - 1), 32 * kJoinWarps, 0, stream, p);
 }
 
-int tiles_of(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// Tiles of 8 pairs where no sequence has more, else of 16.  Two sequences of 16,384
+// rows, 16 heads of 128, with tiles of 8 / 16 / 32 pairs: 8 pairs take 33 / 47 / 69 us,
+// 16 pairs 51 / 49 / 70 us, 32 pairs 88 / 68 / 72 us (a tile of 32 leaves one block
+// on an SM; two of 16 read the codes again, from L2).
+int tiles_of(long long pairs) { return pairs <= 8 ? 1 : 2; }
 
 }  // namespace
 
-size_t cache_rows_partial_bytes(int d, long long rows) {
-  return (size_t)2 * kGrid * 8 * tiles_of(rows) * (d + 2) * sizeof(float);
+size_t cache_rows_partial_bytes(int d, long long pairs) {
+  return (size_t)2 * kGrid * 8 * tiles_of(pairs) * (d + 2) * sizeof(float);
 }
 
-cudaError_t launch_cache_rows(const CacheAttnParams& p, long long rows, cudaStream_t stream) {
-  switch (tiles_of(rows)) {
-    case 1: return p.c.d == 64 ? launch_t<64, 1>(p, stream) : launch_t<128, 1>(p, stream);
-    case 2: return p.c.d == 64 ? launch_t<64, 2>(p, stream) : launch_t<128, 2>(p, stream);
-    default: return p.c.d == 64 ? launch_t<64, 4>(p, stream) : launch_t<128, 4>(p, stream);
-  }
+cudaError_t launch_cache_rows(const CacheAttnParams& p, long long pairs, cudaStream_t stream) {
+  if (tiles_of(pairs) == 1) return p.c.d == 64 ? launch_t<64, 1>(p, stream) : launch_t<128, 1>(p, stream);
+  return p.c.d == 64 ? launch_t<64, 2>(p, stream) : launch_t<128, 2>(p, stream);
 }
 
 }  // namespace h3
