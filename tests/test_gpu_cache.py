@@ -314,6 +314,30 @@ def test_forward_with_strong_scores(rows):
 
 
 @pytest.mark.parametrize("rows", [1, 40, 300])
+def test_forward_with_scores_of_millions(rows):
+    """Scores 127 2^15 (4.2 million) apart from the next by 2^15 or more: each row gets its best key's value.  The
+    probability's rounding to 16 bits and the output's are 2^-8 of the value each; the score is a product of fp32
+    factors with at most eight roundings of 2^-24 up to the normaliser."""
+    L, d = 700, 64
+    g = torch.Generator().manual_seed(8)
+    k = torch.zeros(11, 1, 64, d, dtype=torch.int8)
+    k[..., 0] = torch.randint(-126, 127, (11, 1, 64), generator=g, dtype=torch.int8)
+    v = torch.randint(-127, 128, (11, 1, 64, d), generator=g, dtype=torch.int8)
+    k[10, 0, 20, 0], k[4, 0, 7, 0] = 127, -127
+    ks, vs = torch.full((11, 1), 2.0 ** -6), 0.005 + 0.03 * torch.rand(11, 1, generator=g)
+    c = h3.Cache(*(x.to(DEV) for x in (k, v, ks, vs)))
+    q = torch.zeros(2, rows, d, dtype=torch.bfloat16)
+    q[0, :, 0], q[1, :, 0] = 2.0 ** 24, -(2.0 ** 24)
+    ws = h3.cache_workspace(c, 2, rows, 1)
+    o, lse = h3.cache_forward(c, q.to(DEV), i32([0, rows]), i32([L]), i32([list(range(11))]), ws=ws, lse=True)
+    assert h3.check(ws) == h3.OK
+    for h, (page, row) in enumerate([(10, 20), (4, 7)]):
+        ref = (v[page, 0, row].double() * vs[page, 0].double()).expand(rows, d)
+        assert torch.all((o[h].cpu().double() - ref).abs() <= (2.0 ** -7 + 2.0 ** -16) * ref.abs())
+        assert torch.all((lse[h].cpu().double() - 127 * 2.0 ** 15).abs() <= 2.0 ** -21 * 127 * 2.0 ** 15)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 300])
 def test_forward_scales_far_apart(rows):
     """Pages whose scales differ by many orders of magnitude, a page of zeros with the smallest scale among them."""
     lengths = [64 * 9]
