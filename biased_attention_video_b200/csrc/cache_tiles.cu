@@ -387,8 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         bool ok = true, warm = false;  // warm: every row of the warp has a running maximum
 
         // The running maximum becomes at least mx - 8; O and l follow by the factor
-        // that is returned, a power of two.
+        // that is returned, a power of two.  TMEM stores are asynchronous, and only
+        // tmem_wait_st() orders a later load of the same columns behind them: it covers
+        // the O that an earlier raise of the same step stored, which is loaded here, and
+        // the probabilities that the step has stored, which the caller loads back.
         auto raise = [&](float mx) -> float {
+          tmem_wait_st();
           const bool grow = mx > m + kRescaleThreshold;
           const bool rescale = grow && m > -INFINITY;
           const float up = rescale ? ceilf(mx - m) : 0.0f;
