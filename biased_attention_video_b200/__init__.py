@@ -479,10 +479,19 @@ def _rows(t, name: str, H, d: int, dev: int):
     return shape[1], h if shape[0] > 1 else 0, r if shape[1] > 1 else 0
 
 
+def _space(ws, dev: int):
+    """The caller's workspace: its address goes to kernels on this device."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {_name(dev)}, not on {ws.device}")
+    return ws
+
+
 def _on(dev: int, stream):
-    """Context in which the cache's device and the call's stream are current."""
+    """Context in which the cache's device and the call's stream, one of that device, are current."""
     if stream is None and dev == torch._C._cuda_getDevice():
         return _HERE
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream must be one of {_name(dev)}, not of cuda:{stream.device_index}")
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(dev))
     if stream is not None:
@@ -510,8 +519,7 @@ def cache_append(c: Cache, k, v, row_start, length, page_table, rope: Optional[R
     if row_times is not None:
         _want(row_times, "row_times", torch.float32, (T,), dev)
     with _on(dev, stream):
-        if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=c.device)
+        ws = torch.zeros(256, dtype=torch.uint8, device=c.device) if ws is None else _space(ws, dev)
         rc = lib().h3attn_cache_append(cs, b, k.data_ptr(), kh, kr, v.data_ptr(), vh, vr,
                                        rope._c if rope is not None else None, _dptr(row_times), ws.data_ptr(),
                                        ws.numel(), _raw_stream(dev))
@@ -536,8 +544,7 @@ def cache_read(c: Cache, row_start, first, page_table, T: Optional[int] = None, 
         if v_out is not None:
             _want(v_out, "v_out", torch.bfloat16, (cs.H, rows, cs.d), dev)
         b = _batch(dev, rows, row_start, first, page_table)
-        if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=c.device)
+        ws = torch.zeros(256, dtype=torch.uint8, device=c.device) if ws is None else _space(ws, dev)
         rc = lib().h3attn_cache_read(cs, b, _dptr(k_out), _dptr(v_out), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     _raise(rc, "cache_read")
     return k_out, v_out
@@ -566,8 +573,7 @@ def cache_forward(c: Cache, q, row_start, length, page_table, causal: bool = Fal
     with _on(dev, stream):
         o = torch.empty((H, T, d), dtype=torch.bfloat16, device=c.device) if out is None else out
         lse_t = lse if given else torch.empty((H, T), dtype=torch.float32, device=c.device) if lse else None
-        if ws is None:
-            ws = cache_workspace(c, H, T, b.B)
+        ws = cache_workspace(c, H, T, b.B) if ws is None else _space(ws, dev)
         rc = lib().h3attn_cache_forward(cs, b, H, max_rows or 0, q.data_ptr(), qh, qr, int(causal), pn, _dptr(q_times),
                                         o.data_ptr(), _dptr(lse_t), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     _raise(rc, "cache_forward")

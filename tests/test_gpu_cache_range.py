@@ -1,11 +1,12 @@
-"""Attention over the paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running
-maxima that rise again and again inside a step."""
+"""The paged int8 cache at the ends of its range: running maxima that rise again and again inside a step (against fp64
+with the bounds of cache_ref); workspaces that are not the device's."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_cache import check_forward, make_cache, make_table
+import biased_attention_video_b200 as h3
+from test_gpu_cache import DEV, check_forward, i32, make_cache, make_table
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,16 @@ def test_maxima_that_jump_between_the_pages_of_a_step(d, rows):
     levels = [-120 + 35 * ((j // 64 + 1) // 2) for j in range(n)]
     c, host, table, queries = ladder(d, levels, 2.0, seed=d + rows)
     check_forward(c, host, table, [n], [rows], 2, q=queries(2, rows))
+
+
+def test_calls_refuse_a_workspace_of_the_host():
+    c, _ = make_cache(2, 1, 64)
+    x = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device=DEV)
+    before = [t.clone() for t in (c.k, c.k_scale)]
+    args = i32([0, 3]), i32([0]), i32([[0]])
+    ws = torch.zeros(1 << 26, dtype=torch.uint8)
+    for call in (lambda: h3.cache_append(c, x, x, *args, ws=ws), lambda: h3.cache_read(c, *args, T=3, ws=ws),
+                 lambda: h3.cache_forward(c, x, *args, ws=ws)):
+        with pytest.raises(ValueError, match="ws must be contiguous on cuda:0, not on cpu"):
+            call()
+    assert torch.equal(c.k, before[0]) and torch.equal(c.k_scale, before[1])
