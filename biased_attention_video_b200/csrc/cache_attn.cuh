@@ -79,6 +79,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// V scales of this range, [2^-60, 2^40], go into the exponent.  Tiles: p vs is then normal for p in
+// [2^-66, 2^60].  Few rows: sums of p / vs stay below 2^(15 + 60 + 30), and a key's p falls below
+// fp32 only when its weight is under 2^-38 of another key's.
+constexpr float kScaleLow = 8.673617379884035e-19f, kScaleHigh = 1099511627776.0f;
+
 __device__ __forceinline__ float log2_approx(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

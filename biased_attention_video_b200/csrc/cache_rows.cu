@@ -24,7 +24,10 @@
 // scaled per row by a power of two to a maximum in [2^9, 2^10) (its 8-bit
 // mantissas stay exact down to 2^-23 of the row's maximum), and the V scale goes
 // into the exponent, so that a probability times its V scale is 2^12 at the row's
-// largest and keeps more bits than bf16 would down to 2^-26 of that.
+// largest and keeps more bits than bf16 would down to 2^-26 of that.  A V scale
+// outside [2^-60, 2^40] (a page of zeros, or one marked as not finite) goes in as
+// the nearest end of that range, and the product with V takes bf16 operands, whose
+// range holds the rest of the scale.
 // The d order of A and of Q agree by construction and nothing else sees it, so
 // a lane takes 16 consecutive bytes of a row per load.  mma.sync and not tcgen05:
 // 8 rows fill no 128-row tile, and the widened codes are in registers anyway.
@@ -105,6 +108,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                                         uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -441,8 +452,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rows_kernel(const Cach
       const float* meta = reinterpret_cast<const float*>(ring + i % kStages * L::kStage + L::kMeta);
       const int live = __float_as_int(meta[2]);
       if (live == 0) continue;
-      // a V scale that is not finite marks the probabilities of the keys that are seen, and only those
-      const float ks = meta[0], vs = meta[1], lv = log2_approx(vs), iv = vs < 3.0e38f ? rcp_approx(vs) : 1.0f;
+      // the V scale's part in the exponent (the lower end for NaN), and what of it stays outside
+      const float ks = meta[0], vs = meta[1], ve = fminf(fmaxf(vs, kScaleLow), kScaleHigh);
+      const float lv = log2_approx(ve), iv = rcp_approx(ve);
       const int key = first + i * (kWarps * kKeys);
 
       // S^T: kKeys keys x 8 NT pairs
@@ -527,50 +539,68 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) rows_kernel(const Cach
             }
           }
       }
-      uint32_t pb[kM][NT][2];
+      // probabilities, and O^T += V^T P^T; `outside`: the scale has a rest
+      auto accumulate = [&](auto outside, float rest) {
+        constexpr bool kOutside = decltype(outside)::value;
+        // a rest that is not finite stays away from pairs that do not see the key
+        auto packed = [&](float a, float b) {
+          if constexpr (kOutside) return pack_bf16(a == 0.0f ? 0.0f : a * rest, b == 0.0f ? 0.0f : b * rest);
+          else return pack_f16(a, b);
+        };
+        auto widened = [&](uint32_t w) {
+          if constexpr (kOutside) return widen2(w);
+          else return widen2h(w);
+        };
+        uint32_t pb[kM][NT][2];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        const float m0 = (m[x][0] == -INFINITY ? 0.0f : m[x][0]) - kShift;
-        const float m1 = (m[x][1] == -INFINITY ? 0.0f : m[x][1]) - kShift;
-        float s0 = 0.0f, s1 = 0.0f;
+        for (int x = 0; x < NT; ++x) {
+          const float m0 = (m[x][0] == -INFINITY ? 0.0f : m[x][0]) - kShift;
+          const float m1 = (m[x][1] == -INFINITY ? 0.0f : m[x][1]) - kShift;
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < kM; ++mt) {
+            const float p0 = ex2(acc[mt][x][0] - m0), p1 = ex2(acc[mt][x][1] - m1);
+            const float p2 = ex2(acc[mt][x][2] - m0), p3 = ex2(acc[mt][x][3] - m1);
+            s0 += p0 + p2;
+            s1 += p1 + p3;
+            pb[mt][x][0] = transpose8x8(packed(p0, p1));
+            pb[mt][x][1] = transpose8x8(packed(p2, p3));
+          }
+          l[x][0] = fmaf(s0, iv, l[x][0]);
+          l[x][1] = fmaf(s1, iv, l[x][1]);
+        }
+        // this lane's keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of a 16, its columns from g D / 8 on
 #pragma unroll
         for (int mt = 0; mt < kM; ++mt) {
-          const float p0 = ex2(acc[mt][x][0] - m0), p1 = ex2(acc[mt][x][1] - m1);
-          const float p2 = ex2(acc[mt][x][2] - m0), p3 = ex2(acc[mt][x][3] - m1);
-          s0 += p0 + p2;
-          s1 += p1 + p3;
-          pb[mt][x][0] = transpose8x8(pack_f16(p0, p1));
-          pb[mt][x][1] = transpose8x8(pack_f16(p2, p3));
-        }
-        l[x][0] = fmaf(s0, iv, l[x][0]);
-        l[x][1] = fmaf(s1, iv, l[x][1]);
-      }
-      // O^T += V^T P^T: this lane's keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of a 16, its columns from g D / 8 on
+          uint32_t v[4][D / 32];
 #pragma unroll
-      for (int mt = 0; mt < kM; ++mt) {
-        uint32_t v[4][D / 32];
+          for (int r = 0; r < 4; ++r) {
+            const int row = 2 * t + (r & 1) + (r >> 1) * 8;
+            const uint32_t a = st + L::kV + (16 * mt + row) * D;
+            if constexpr (D == 128) {
+              const uint4 x = lds128(a + ((g ^ ((row >> 1 & 3) << 1)) << 4));
+              v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+            } else {
+              const uint2 x = lds64(a + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
+              v[r][0] = x.x, v[r][1] = x.y;
+            }
+          }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 2 * t + (r & 1) + (r >> 1) * 8;
-          const uint32_t a = st + L::kV + (16 * mt + row) * D;
-          if constexpr (D == 128) {
-            const uint4 x = lds128(a + ((g ^ ((row >> 1 & 3) << 1)) << 4));
-            v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-          } else {
-            const uint2 x = lds64(a + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8);
-            v[r][0] = x.x, v[r][1] = x.y;
+          for (int j = 0; j < kJ; ++j) {
+            const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+            const uint32_t ab = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel);
+            const uint32_t cd = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
+            const uint32_t a0 = widened(ab), a1 = widened(ab >> 8), a2 = widened(cd), a3 = widened(cd >> 8);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              if constexpr (kOutside) mma_bf16(o[x][j], a0, a1, a2, a3, pb[mt][x][0], pb[mt][x][1]);
+              else mma_f16(o[x][j], a0, a1, a2, a3, pb[mt][x][0], pb[mt][x][1]);
+            }
           }
         }
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-          const uint32_t ab = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel);
-          const uint32_t cd = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
-          const uint32_t a0 = widen2h(ab), a1 = widen2h(ab >> 8), a2 = widen2h(cd), a3 = widen2h(cd >> 8);
-#pragma unroll
-          for (int x = 0; x < NT; ++x) mma_f16(o[x][j], a0, a1, a2, a3, pb[mt][x][0], pb[mt][x][1]);
-        }
-      }
+      };
+      if (ve == vs) accumulate(std::false_type{}, 1.0f);
+      else accumulate(std::true_type{}, vs * iv);
     }
     __syncwarp();  // the ring is read
 

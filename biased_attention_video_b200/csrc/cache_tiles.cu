@@ -230,8 +230,6 @@ struct PageMeta {
   float t;
   int plain;    // 64 valid keys, V scale in the range in which it goes into the exponent
 };
-// V scales in [2^-60, 2^40] go into the exponent: p vs is then normal for p in [2^-66, 2^kStale].
-constexpr float kScaleLow = 8.673617379884035e-19f, kScaleHigh = 1099511627776.0f;
 // A score may exceed the running maximum by this much (log2 units) before the
 // maximum is brought up: probabilities, sums and O are floating point, so a stale
 // maximum costs no accuracy, and one pass over the scores is enough.  (Probabilities

@@ -322,8 +322,8 @@ H3ATTN_API int h3attn_dense_biased(int H, int S, int d, const uint16_t* q, const
  *
  * A page is one block of 64 consecutive rows of one sequence, all K/V heads:
  *  k, v: int8 codes [n_pages][H][64][d]; k_scale, v_scale: float32
- *  [n_pages][H]; value = code * scale of its page and head.  d 64 or 128,
- *  block 64, k and v 16-byte aligned, scales 4-byte.
+ *  [n_pages][H], not negative; value = code * scale of its page and head.
+ *  d 64 or 128, block 64, k and v 16-byte aligned, scales 4-byte.
  *  times: float32 [n_pages][64] (16-byte aligned) or NULL: the rows' guide times
  *  in seconds for the temporal penalty, NaN for a row that is no guide row.
  * Plain data; the caller owns the buffers.  No initial contents are needed: a
@@ -390,7 +390,8 @@ H3ATTN_API size_t h3attn_cache_workspace_bytes(const h3attn_cache* cache, int H,
  *   code = clamp(rint(y * (1 / s')), -127, 127);
  * earlier rows of a page whose scale grows are taken along:
  * code' = rint(code * (s / s')).  A value that is not finite gives the page and
- * head the scale NaN, and attention over the page is NaN.
+ * head the scale NaN: O of the rows that see the page is NaN, and for a key so is
+ * their LSE.
  * Rows of a page from position length[b] on are replaced and the ones behind
  * the new rows are undefined: appending at a smaller length drops what was there.
  * row_times: float32 [T] guide times (NaN: no guide row), or NULL for none;

@@ -1,5 +1,5 @@
-"""The paged int8 cache at the ends of its range: running maxima that rise again and again inside a step (against fp64
-with the bounds of cache_ref); workspaces that are not the device's."""
+"""The paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running maxima that rise
+again and again inside a step, V scales from nothing to 1e30, long caches of zeros; workspaces that are not the device's."""
 import math
 
 import pytest
@@ -69,3 +69,72 @@ def test_calls_refuse_a_workspace_of_the_host():
         with pytest.raises(ValueError, match="ws must be contiguous on cuda:0, not on cpu"):
             call()
     assert torch.equal(c.k, before[0]) and torch.equal(c.k_scale, before[1])
+
+
+V_SCALES = {  # pages of a sequence; what lies between is ordinary
+    "pages of zero": {0: 0.0, 3: 0.0, 8: 0.0},
+    "all zero": dict.fromkeys(range(9), 0.0),
+    "below the smallest normal": {1: 2.0 ** -140, 4: 2.0 ** -149, 8: 2.0 ** -127},
+    "about the ends": {0: 2.0 ** -61, 1: 2.0 ** -60, 2: 2.0 ** -59, 3: 0.0, 8: 2.0 ** -62},
+    "all tiny": dict.fromkeys(range(9), 2.0 ** -80),
+    "large": {2: 2.0 ** 39, 3: 2.0 ** 41, 8: 2.0 ** 40},
+    "huge": {2: 1e30, 5: 0.0},
+    "huge at the end": {8: 1e30},
+}
+
+
+@pytest.mark.parametrize("scales", list(V_SCALES))
+@pytest.mark.parametrize("d,rows,causal", [(64, 1, False), (128, 1, False), (128, 5, True), (64, 16, True), (128, 150, True),
+                                           (64, 150, False)])
+def test_values_of_any_scale(scales, d, rows, causal):
+    """A key counts in the normaliser whatever its value's scale; causal rows see less than the last page."""
+    lengths = [64 * 8 + 50]
+    c, host = make_cache(9, 1, d, seed=d + rows)
+    table = make_table(lengths, 9)
+    for p, scale in V_SCALES[scales].items():
+        host[3][table[0][p], 0] = scale
+    c.v_scale.copy_(host[3])
+    check_forward(c, host, table, lengths, [rows], 2, causal=causal, seed=rows)
+
+
+@pytest.mark.parametrize("d,H,rows", [(64, 1, 1), (128, 2, 7), (64, 2, 40)])
+def test_a_long_cache_of_zeros(d, H, rows):
+    """131,072 rows of zero keys and values: O = 0 and LSE = log 131072.  The sums are powers of two and exact; the
+    logarithm of the scale has a relative error of 2^-22 of at most 60, what follows a few roundings of 2^-24 of 89."""
+    n = 1 << 17
+    c = h3.Cache.empty(n // 64, 1, d)
+    table = torch.randperm(n // 64, device=DEV).to(torch.int32)[None]
+    ws = h3.cache_workspace(c, H, rows, 1)
+    x = torch.zeros(1, n, d, dtype=torch.bfloat16, device=DEV)
+    h3.cache_append(c, x, x, i32([0, n]), i32([0]), table, ws=ws)
+    q = torch.randn(H, rows, d, device=DEV).to(torch.bfloat16)
+    o, lse = h3.cache_forward(c, q, i32([0, rows]), i32([n]), table, ws=ws, lse=True)
+    assert h3.check(ws) == h3.OK
+    assert torch.all(o == 0) and torch.all((lse - math.log(n)).abs() <= 2.0 ** -15)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_long_cache_whose_first_page_is_lower(rows):
+    """116,883 rows of zero values; all but the first page lie 2^2 above it, less than what raises the few-row kernel's
+    maximum, so the normaliser's terms stay four times larger than at their maximum."""
+    n = 116883
+    c, host, table, queries = ladder(64, [0 if j < 64 else 100 for j in range(n)], 0.02, scale=0.0)
+    q = queries(1, rows)
+    q[:, :, 1:] = 0
+    check_forward(c, host, table, [n], [rows], 1, q=q)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 150])
+def test_marked_values_leave_the_normaliser(rows):
+    """A V scale of NaN makes the output NaN and leaves LSE as it is; a K scale of NaN makes both NaN."""
+    c, _ = make_cache(3, 1, 128, seed=2)
+    q = torch.randn(2, rows, 128, device=DEV).to(torch.bfloat16)
+    args = q, i32([0, rows]), i32([130]), i32([[0, 1, 2]])
+    _, want = h3.cache_forward(c, *args, lse=True)
+    c.v_scale[1, 0] = float("nan")
+    o, lse = h3.cache_forward(c, *args, lse=True)
+    # the same scores and sums, in another order of roundings of 2^-24 and with the scale's logarithm (2^-22 of 60)
+    assert torch.all(torch.isnan(o)) and torch.all((lse - want).abs() <= 2.0 ** -15)
+    c.k_scale[1, 0] = float("nan")
+    o, lse = h3.cache_forward(c, *args, lse=True)
+    assert torch.all(torch.isnan(o)) and torch.all(torch.isnan(lse))
