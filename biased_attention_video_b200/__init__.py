@@ -555,8 +555,9 @@ def cache_forward(c: Cache, q, row_start, length, page_table, causal: bool = Fal
                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Attention of packed query rows q bf16 [H, T, d] over the cached rows [0, length[b]) of their sequence
     (h3attn_cache_forward); (o, lse) is one partition for merge().  The penalty needs q_times (float32 [T], NaN for
-    rows without one) and the cache's times.  Rows of a new ``out`` that belong to no sequence are not written.  Scores must
-    stay below 2^23 in magnitude; beyond, the result is undefined."""
+    rows without one) and the cache's times.  Rows of a new ``out`` that belong to no sequence are not written.  q . k /
+    sqrt(d) and each row's largest score, penalty included, must stay below 2^23 in magnitude; beyond, the result is
+    undefined."""
     cs = c._c
     dev = c._t[0].get_device()
     T, qh, qr = _rows(q, "q", None, cs.d, dev)

@@ -2,6 +2,8 @@
 // launches.  See the cache section of include/h3attn.h for the contract.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -145,9 +147,12 @@ int h3attn_cache_forward(const h3attn_cache* cache, const h3attn_batch* batch, i
       const float log2e = 1.4426950408889634f;
       p.q_times = q_times;
       p.window = pen->window;
-      p.inv_falloff = 1.0f / pen->falloff;
-      p.strength_log2 = pen->strength * log2e;
-      p.cap_log2 = pen->cap * log2e;
+      // An infinite factor would make 0 inf of a key inside the window.  A penalty of 2^26
+      // (log2 units) leaves nothing of a key beside one without, for scores lie within 2^24;
+      // maxima of masked keys then still have an ulp of 8, far inside the kernels' margins.
+      p.inv_falloff = std::min(1.0f / pen->falloff, FLT_MAX);
+      p.strength_log2 = std::min(pen->strength * log2e, FLT_MAX);
+      p.cap_log2 = std::min(pen->cap * log2e, 67108864.0f);
     }
   }
   if (p.b.T == 0) return H3ATTN_OK;

@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
             };
             // one page with the running maximum as it is; false if a score exceeds it by 2^kStale
             auto page = [&](int col, const PageMeta& pg, float pen, bool more) -> bool {
-              const float off = pg.lv - m - pen;
+              const float off = pg.lv - (m + pen);  // m + pen first: both may be large
               tmem_landed(x);
               load32(y, col + 32);
               float top = top32(x), s = probs32(x, off, pg.c, pk);

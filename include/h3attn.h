@@ -417,8 +417,11 @@ H3ATTN_API int h3attn_cache_read(const h3attn_cache* cache, const h3attn_batch* 
  * row that both have a time (q_times float32 [T], NaN for a row that is no
  * output row; cache->times).  A row that sees no key gets O = 0 and LSE = -inf,
  * so that o and lse are one partition for h3attn_merge with any others.
- * Scores must stay below 2^23 in magnitude: larger ones are further apart in
- * fp32 than a softmax can tell, and the result is then undefined.
+ * q . k / sqrt(d) must stay below 2^23 in magnitude, and so must each row's
+ * largest score, penalty included: larger ones are further apart in fp32 than a
+ * softmax can tell, and the result is then undefined.  Below a row's largest
+ * score any finite penalty is right (it counts as 4.6e7 at most): a cap of 1e9
+ * masks the keys beyond the window.
  * q: bf16 by strides, as k above; o: bf16 [H][T][d], 16-byte aligned; lse:
  * float32 [H][T] natural-log normaliser or NULL.  Rows that belong to no
  * sequence are left as they were.

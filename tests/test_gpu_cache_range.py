@@ -1,5 +1,5 @@
 """The paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running maxima that rise
-again and again inside a step, V scales from nothing to 1e30, long caches of zeros; workspaces that are not the device's."""
+again and again inside a step, V scales from nothing to 1e30, long caches of zeros, penalties that mask; workspaces that are not the device's."""
 import math
 
 import pytest
@@ -69,6 +69,24 @@ def test_calls_refuse_a_workspace_of_the_host():
         with pytest.raises(ValueError, match="ws must be contiguous on cuda:0, not on cpu"):
             call()
     assert torch.equal(c.k, before[0]) and torch.equal(c.k_scale, before[1])
+
+
+@pytest.mark.parametrize("cap", [1e9, 1e10, 3e38])
+@pytest.mark.parametrize("rows,one_time", [(1, True), (12, False), (40, True), (300, True), (300, False)])
+def test_penalty_as_a_mask(cap, rows, one_time):
+    """Every key outside the window is masked by the cap; a row's first keys are, and what it does see has scores of
+    several hundred.  With one_time pages of one guide time, else the keys of a page alternate between two."""
+    n = 64 * 10 + 20
+    c, host = make_cache(11, 1, 128, seed=rows, times=True)
+    table = make_table([n], 11, seed=rows)
+    for i, p in enumerate(table[0]):  # the queries' times are multiples of 0.17 up to 1.87, or none
+        host[4][p] = 5.0 if i < 6 else 0.17 * (i % 3)
+        if not one_time:
+            host[4][p, ::2] = 5.0
+        if i == 8:
+            host[4][p] = float("nan")
+    c.times.copy_(host[4])
+    check_forward(c, host, table, [n], [rows], 2, pen=(cap, 2.0, 0.01, cap), q_scale=60.0, seed=rows)
 
 
 V_SCALES = {  # pages of a sequence; what lies between is ordinary
