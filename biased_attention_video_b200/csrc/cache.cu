@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) append_kernel(const Ap
       const int r = i / quads, q = i % quads;
       int pos = p.rope.index != nullptr ? __ldg(p.rope.index + pc.row + r) : pc.lo + r;
       if (pos < 0 || pos >= p.rope.n_pos) {
-        cache_report(p.status, kStatusData);
+        report(p.status, kStatusData);
         pos = min(max(pos, 0), p.rope.n_pos - 1);
       }
       reinterpret_cast<float4*>(tab_w.cos[r])[q] = __ldg(reinterpret_cast<const float4*>(p.rope.cos + (size_t)pos * half) + q);

@@ -83,8 +83,6 @@ cudaError_t launch_cache_tiles(const CacheAttnParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------ device side
 
-__device__ __forceinline__ void cache_report(int* status, int code) { atomicCAS(status, 0, code); }
-
 // Rows [first, first + n) of sequence b in the packed rows, forced into [0, T]
 // (offsets that are not ascending in [0, T] are reported).
 struct SeqRows {
@@ -93,7 +91,7 @@ struct SeqRows {
 __device__ __forceinline__ SeqRows seq_rows(const BatchRef& r, int b, int* status) {
   const int a = __ldg(r.row_start + b), e = __ldg(r.row_start + b + 1);
   const int first = min(max(a, 0), r.T), last = min(max(e, first), r.T);
-  if (first != a || last != e) cache_report(status, kStatusData);
+  if (first != a || last != e) report(status, kStatusData);
   return SeqRows{first, last - first};
 }
 
@@ -101,7 +99,7 @@ __device__ __forceinline__ SeqRows seq_rows(const BatchRef& r, int b, int* statu
 __device__ __forceinline__ int seq_length(const BatchRef& r, int b, int* status) {
   const int n = __ldg(r.length + b);
   const int held = min(max(n, 0), r.max_pages * kBlock);
-  if (held != n) cache_report(status, kStatusData);
+  if (held != n) report(status, kStatusData);
   return held;
 }
 
@@ -132,7 +130,7 @@ __device__ __forceinline__ Piece find_piece(const BatchRef& r, int x, int* statu
         start[e] = seq_length(r, b, status);
         first[e] = s.first;
         n[e] = min(s.n, r.max_pages * kBlock - start[e]);
-        if (n[e] < s.n) cache_report(status, kStatusData);
+        if (n[e] < s.n) report(status, kStatusData);
         cnt[e] = n[e] > 0 ? (start[e] + n[e] - 1) / kBlock - start[e] / kBlock + 1 : 0;
       }
       mine += cnt[e];
@@ -186,7 +184,7 @@ inline unsigned max_pieces(const BatchRef& r) {
 __device__ __forceinline__ int page_id(const CacheRef& c, const BatchRef& r, int b, int page_no, int* status) {
   const int id = __ldg(r.page_table + (size_t)b * r.max_pages + page_no);
   if (id < 0 || id >= c.n_pages) {
-    cache_report(status, kStatusData);
+    report(status, kStatusData);
     return -1;
   }
   return id;

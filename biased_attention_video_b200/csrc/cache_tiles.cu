@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         const int no = (step0 + j) * 2 + page_of;
         page = entry;
         if (j < n && no * kBlock < it.len && (page < 0 || page >= p.c.n_pages)) {
-          cache_report(p.status, kStatusData);
+          report(p.status, kStatusData);
           page = -1;
         }
         read_entry(j + 1);

@@ -16,6 +16,13 @@ constexpr int kMaxSmem = 227 * 1024;  // opt-in dynamic shared memory of one CTA
 constexpr int kStatusTimeout = 1;
 constexpr int kStatusData = 2;
 
+// Records a code in the status word.  Of bad values the first one stays; a wait
+// that gave up overwrites it, for then the output is incomplete.
+__device__ __forceinline__ void report(int* status, int code) {
+  if (code == kStatusTimeout) atomicExch(status, code);
+  else atomicCAS(status, 0, code);
+}
+
 struct AttnParams {
   int H, S, d;
   int n_blocks, first_video_block, n_video_blocks, k;

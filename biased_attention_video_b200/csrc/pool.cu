@@ -125,7 +125,7 @@ __global__ void selftest_timeout_kernel(int* status, uint32_t polls) {
     fence_mbar_init();
     bool done = false;
     for (uint32_t i = 0; i < polls && !done; ++i) done = mbar_try_wait(&bar, 0);
-    if (!done) atomicCAS(status, 0, kStatusTimeout);
+    if (!done) report(status, kStatusTimeout);
   }
 }
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t parity, volati
       if (t0 == 0) t0 = now;
       if (now - t0 > 2000000000ull) {
         *abort = 1;
-        if (status != nullptr) atomicCAS(status, 0, kStatusTimeout);
+        if (status != nullptr) report(status, kStatusTimeout);
         return false;
       }
     }
@@ -166,7 +166,7 @@ __device__ __forceinline__ void gemm_drain(uint64_t* bar, uint32_t parity, int* 
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
       if (t0 == 0) t0 = now;
       if (now - t0 > 2000000000ull) {
-        if (status != nullptr) atomicCAS(status, 0, kStatusTimeout);
+        if (status != nullptr) report(status, kStatusTimeout);
         return;
       }
     }

@@ -25,8 +25,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void report(int* status, int code) { atomicCAS(status, 0, code); }
-
 // Bounded wait with CTA-wide abort.  On give-up: raise the CTA abort flag and
 // the global status word.
 template <class Params>

@@ -146,7 +146,7 @@ __device__ __forceinline__ bool tail_wait(uint64_t* bar, uint32_t parity, int* s
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
       if (t0 == 0) t0 = now;
       if (now - t0 > 2000000000ull) {
-        if (status != nullptr) atomicCAS(status, 0, kStatusTimeout);
+        if (status != nullptr) report(status, kStatusTimeout);
         return false;
       }
     }

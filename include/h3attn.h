@@ -434,8 +434,8 @@ H3ATTN_API int h3attn_cache_forward(const h3attn_cache* cache, const h3attn_batc
                                     size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return and clear the device-side status word
- * of ws: H3ATTN_OK, H3ATTN_ETIMEOUT or H3ATTN_EDATA; H3ATTN_ECUDA if the
- * stream reports an error. */
+ * of ws: H3ATTN_OK, H3ATTN_ETIMEOUT or H3ATTN_EDATA (ETIMEOUT where both
+ * were recorded); H3ATTN_ECUDA if the stream reports an error. */
 H3ATTN_API int h3attn_check(void* ws, void* stream);
 
 /* Test and diagnostics only: bound every device-side wait of the attention

@@ -1,5 +1,6 @@
 """The paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running maxima that rise
-again and again inside a step, V scales from nothing to 1e30, long caches of zeros, penalties that mask; workspaces that are not the device's."""
+again and again inside a step, V scales from nothing to 1e30, long caches of zeros, penalties that mask;
+workspaces that are not the device's; what the status word keeps."""
 import math
 
 import pytest
@@ -156,3 +157,20 @@ def test_marked_values_leave_the_normaliser(rows):
     c.k_scale[1, 0] = float("nan")
     o, lse = h3.cache_forward(c, *args, lse=True)
     assert torch.all(torch.isnan(o)) and torch.all(torch.isnan(lse))
+
+
+def test_a_give_up_is_not_hidden_by_bad_data():
+    """A bad page id is recorded first; then a wait that runs out on the same workspace (one that nothing arrives at),
+    which says more: its output is incomplete.  The other way round the give-up stays."""
+    c, _ = make_cache(2, 1, 64)
+    x = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    bad = i32([0, 3]), i32([0]), i32([[7]])
+    h3.cache_append(c, x, x, *bad, ws=ws)
+    assert h3.check(ws) == h3.EDATA
+    h3.cache_append(c, x, x, *bad, ws=ws)
+    h3.selftest_timeout(ws, 100)
+    assert h3.check(ws) == h3.ETIMEOUT
+    h3.selftest_timeout(ws, 100)
+    h3.cache_append(c, x, x, *bad, ws=ws)
+    assert h3.check(ws) == h3.ETIMEOUT and h3.check(ws) == h3.OK
