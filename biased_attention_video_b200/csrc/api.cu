@@ -18,9 +18,8 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
-constexpr uint32_t kWaitPolls = 0xFFFFFFFFu;  // no poll bound: only the time bound applies
 // poll bound of the attention kernels' waits for the calls launched next
-// (h3attn_set_wait_polls; 0 = kWaitPolls)
+// (h3attn_set_wait_polls; 0 = no limit)
 std::atomic<uint32_t> g_wait_polls{0u};
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait: far above any legitimate stall
 using h3::kMaxSmem;
@@ -208,7 +207,7 @@ int forward_impl(const h3attn_plan* plan, const uint16_t* q, const uint16_t* k, 
 namespace h3 {
 uint32_t wait_poll_limit() {
   const uint32_t polls = g_wait_polls.load(std::memory_order_relaxed);
-  return polls == 0u ? kWaitPolls : polls;
+  return polls == 0u ? kNoPollLimit : polls;
 }
 uint64_t wait_time_limit_ns() { return kWaitNs; }
 

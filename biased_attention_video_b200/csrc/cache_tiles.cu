@@ -255,15 +255,18 @@ struct TilesLayout {
 };
 
 // wait_bar by a whole warp, with one answer
-template <class Params>
+template <bool kSuspend, class Params>
 __device__ __forceinline__ bool wait_bar_all(uint64_t* bar, uint32_t parity, const Params& p, volatile int* abort) {
-  return __all_sync(kFull, wait_bar(bar, parity, p, abort));
+  return __all_sync(kFull, wait_bar<kSuspend>(bar, parity, p, abort));
 }
 
 // The whole block, from roles that run different code.
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
-template <int D, bool kPen>
+// kSuspend false: for calls with a poll limit (h3attn_set_wait_polls), whose polls must
+// not suspend: one that does outlasts every wait here, so that no limit would run out.
+// (One kernel that looks at the limit at every wait is 8 to 13 % slower.)
+template <int D, bool kPen, bool kSuspend>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParams p) {
   using L = TilesLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t q = done + j, mine = (sub ? done_b : done) + j;  // steps, and steps of this tile
           const int slot = q & 3;
-          ok = __all_sync(kFull, wait_bar(m_full + slot, (q >> 2) & 1u, p, abort_flag));
+          ok = wait_bar_all<kSuspend>(m_full + slot, (q >> 2) & 1u, p, abort_flag);
           if (!ok) break;
           const PageMeta* meta = reinterpret_cast<const PageMeta*>(smem + L::kMeta) + 2 * slot;
           const PageMeta pa = meta[0], pb = meta[1];
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           const bool plain = pa.plain && pb.plain && key0 + kStep <= lim_all;
           const float pen_a = kPen && pa.mode == 1 ? block_penalty_log2(tq, pa.t, p) : 0.0f;
           const float pen_b = kPen && pb.mode == 1 ? block_penalty_log2(tq, pb.t, p) : 0.0f;
-          ok = __all_sync(kFull, wait_bar(s_full + 2 * sub + (mine & 1u), (mine >> 1) & 1u, p, abort_flag));
+          ok = wait_bar_all<kSuspend>(s_full + 2 * sub + (mine & 1u), (mine >> 1) & 1u, p, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (plain) {
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
           if (lane == 0) mbar_arrive(p_full + sub);
         }
         // ------------------------------------------------------- output
-        if (ok) ok = __all_sync(kFull, wait_bar(o_final, items & 1u, p, abort_flag));
+        if (ok) ok = wait_bar_all<kSuspend>(o_final, items & 1u, p, abort_flag);
         if (ok) {
           tc_fence_after();
           const bool whole = n == it.steps;
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         // step's scores may be complete as well by now, but not the next one's.)
         if (j > 0) {
           const uint32_t last = (subs == 2 ? done_b : done) + j - 1;
-          if (!wait_bar_all(s_full + 2 * (subs - 1) + (last & 1u), (last >> 1) & 1u, p, abort_flag)) break;
+          if (!wait_bar_all<kSuspend>(s_full + 2 * (subs - 1) + (last & 1u), (last >> 1) & 1u, p, abort_flag)) break;
         }
         widen(smem + L::kV + s * L::kBlockBytes, vr);
         fence_proxy_async_smem();
@@ -718,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         }
         umma_commit_one(s_full + 2 * sub + (x & 1u));
       };
-      auto wait_k = [&](int j) { return wait_bar_all(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag); };
-      bool ok = wait_bar_all(q_full, items & 1u, p, abort_flag) && wait_k(0);
+      auto wait_k = [&](int j) { return wait_bar_all<kSuspend>(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag); };
+      bool ok = wait_bar_all<kSuspend>(q_full, items & 1u, p, abort_flag) && wait_k(0);
       if (ok) {
         tc_fence_after();
         for (int sub = 0; sub < subs; ++sub) issue_s(sub, 0);
@@ -729,9 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         const bool more = j + 1 < n;
         // the keys of the next step, and with them this step's values: a widening
         // warp stores the values of a step before the keys of the next
-        ok = more ? wait_k(j + 1) : wait_bar_all(v_full, items & 1u, p, abort_flag);
+        ok = more ? wait_k(j + 1) : wait_bar_all<kSuspend>(v_full, items & 1u, p, abort_flag);
         for (int sub = 0; ok && sub < subs; ++sub) {
-          ok = wait_bar_all(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
+          ok = wait_bar_all<kSuspend>(p_full + sub, ((sub ? done_b : done) + j) & 1u, p, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -847,7 +850,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_tiles_kernel(const CacheAtt
 template <int D>
 cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
   constexpr int bytes = TilesLayout<D>::kBytes;
-  auto kernel = p.q_times != nullptr ? tiles_kernel<D, true> : tiles_kernel<D, false>;
+  const bool limit = p.wait_polls != kNoPollLimit;
+  auto kernel = p.q_times != nullptr ? limit ? tiles_kernel<D, true, false> : tiles_kernel<D, true, true>
+                                     : limit ? tiles_kernel<D, false, false> : tiles_kernel<D, false, true>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, 1024, 0, stream>>>(p);

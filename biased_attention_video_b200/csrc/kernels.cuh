@@ -153,6 +153,7 @@ cudaError_t launch_merge(const MergeParts& parts, long long rows, int d, uint16_
                          cudaStream_t stream);
 
 // Bounds of every device-side wait of the calls launched next (h3attn_set_wait_polls).
+constexpr uint32_t kNoPollLimit = 0xFFFFFFFFu;  // only the time bound applies
 uint32_t wait_poll_limit();
 uint64_t wait_time_limit_ns();
 

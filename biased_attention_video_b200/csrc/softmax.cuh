@@ -26,12 +26,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Bounded wait with CTA-wide abort.  On give-up: raise the CTA abort flag and
-// the global status word.
-template <class Params>
+// the global status word.  kSuspend: a poll may itself wait, for a time that the
+// hardware sets.
+template <bool kSuspend = true, class Params>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Params& p, volatile int* abort) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (kSuspend ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
     if (*abort) return false;
     bool give_up = i >= p.wait_polls;
     if ((i & 1023u) == 1023u) {

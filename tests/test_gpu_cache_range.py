@@ -1,6 +1,6 @@
 """The paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running maxima that rise
 again and again inside a step, V scales from nothing to 1e30, long caches of zeros, penalties that mask;
-workspaces that are not the device's; what the status word keeps."""
+workspaces that are not the device's; what the status word keeps; waits that run out."""
 import math
 
 import pytest
@@ -174,3 +174,34 @@ def test_a_give_up_is_not_hidden_by_bad_data():
     h3.selftest_timeout(ws, 100)
     h3.cache_append(c, x, x, *bad, ws=ws)
     assert h3.check(ws) == h3.ETIMEOUT and h3.check(ws) == h3.OK
+
+
+@pytest.mark.parametrize("d,rows,length,pen", [(128, 300, 2000, False), (64, 40, 100, False), (128, 1500, 900, True),
+                                               (64, 300, 4000, True)])
+def test_tiles_give_up_and_recover(d, rows, length, pen):
+    """Every wait of the tile kernel bounded to one poll, which does not suspend: the first wait for rows from memory runs
+    out, the block's roles leave, and the word says so, also when a bad page was recorded.  With larger limits roles leave
+    at other steps, or none does and the output is whole.  Each time the next call on the same workspace is right."""
+    c, host = make_cache(length // 64 + 3, 2, d, seed=21, times=pen)
+    table = make_table([length], length // 64 + 3, width=length // 64 + 2)
+    ws = h3.cache_workspace(c, 2, rows, 1)
+    q = torch.randn(2, rows, d, device=DEV).to(torch.bfloat16)
+    more = dict(pen=h3.DEFAULT_PENALTY, q_times=torch.rand(rows, device=DEV)) if pen else {}
+    args = q, i32([0, rows]), i32([length]), i32(table)
+    want, _ = h3.cache_forward(c, *args, **more)
+
+    def bounded(polls, page_table):
+        try:
+            h3.set_wait_polls(polls)
+            o, _ = h3.cache_forward(c, *args[:3], page_table, ws=ws, **more)
+            return o, h3.check(ws)
+        finally:
+            h3.set_wait_polls(0)
+
+    bad = table.copy()
+    bad[0][0] = -1
+    for polls, page_table in [(1, table), (1, bad), (3, table), (10, table), (30, table), (100, table), (1000, table)]:
+        o, status = bounded(polls, i32(page_table))
+        assert status == h3.ETIMEOUT or (polls > 1 and status == h3.OK and torch.equal(o, want)), polls
+        o, _ = h3.cache_forward(c, *args, ws=ws, **more)
+        assert h3.check(ws) == h3.OK and torch.equal(o, want), polls
