@@ -29,8 +29,10 @@ int check_cache(const h3attn_cache* c, h3::CacheRef* out) {
 
 int check_batch(const h3attn_batch* b, h3::BatchRef* out) {
   if (b == nullptr || b->B < 1 || b->T < 0 || b->max_pages < 1) return H3ATTN_EINVAL;
-  // positions and packed rows are 32-bit, with room for a tile past the end
-  if (b->T > (1 << 30) || b->B > (1 << 24) || b->max_pages > (1 << 24)) return H3ATTN_EUNSUPPORTED;
+  // Positions and packed rows are 32-bit, with room for a tile past the end.  Each block finds
+  // its rows by a scan over the sequences (140 take a microsecond; appending a token of each of
+  // 65,536 takes 35 ms), so B is bounded: 2^24 sequences would hold the GPU for half an hour.
+  if (b->T > (1 << 30) || b->B > (1 << 16) || b->max_pages > (1 << 24)) return H3ATTN_EUNSUPPORTED;
   if (!b->row_start || !b->length || !b->page_table) return H3ATTN_EINVAL;
   if (misaligned(b->row_start, 4) || misaligned(b->length, 4) || misaligned(b->page_table, 4)) return H3ATTN_EALIGN;
   *out = h3::BatchRef{b->B, b->T, b->max_pages, b->row_start, b->length, b->page_table};

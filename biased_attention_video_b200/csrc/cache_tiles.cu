@@ -157,13 +157,13 @@ struct Item {
 __device__ __forceinline__ Item find_item(const CacheAttnParams& p, long long u) {
   const int lane = threadIdx.x & 31;
   Item it;
-  int b = 0;
-  for (int b0 = 0; b0 < p.b.B; b0 += 32) {
-    const unsigned in = __ballot_sync(kFull, b0 + lane < p.b.B && p.base[b0 + lane] <= u && u < p.base[b0 + lane + 1]);
-    if (in != 0u) {
-      b = b0 + __ffs(in) - 1;
-      break;
-    }
+  int b = 0;  // the last sequence whose line begins at or before u; base ascends
+  for (int span = p.b.B; span > 1;) {
+    const int step = (span + 31) / 32, at = b + lane * step;
+    const unsigned in = __ballot_sync(kFull, lane * step < span && p.base[at] <= u);
+    const int last = in != 0u ? 31 - __clz(in) : 0;
+    b += last * step;
+    span = min(step, span - last * step);
   }
   const Seq s = load_seq(p, b);
   const long long lo = p.base[b], per_head = (p.base[b + 1] - lo) / p.c.H;

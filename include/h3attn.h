@@ -337,8 +337,8 @@ typedef struct {
   float* times;
 } h3attn_cache;
 
-/* The sequences of one call over the cache.  Their rows are packed: sequence b
- * has rows [row_start[b], row_start[b + 1]) of T (row_start int32 [B + 1],
+/* The sequences of one call over the cache, at most 65,536.  Their rows are packed:
+ * sequence b has rows [row_start[b], row_start[b + 1]) of T (row_start int32 [B + 1],
  * ascending in [0, T]; rows behind row_start[B] belong to no sequence and are
  * neither read nor written).  length: int32 [B], cached rows (see each call).
  * page_table: int32 [B][max_pages]: row j of sequence b is row j % 64 of page

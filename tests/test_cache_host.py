@@ -42,7 +42,7 @@ BAD_CACHE = [(dict(n_pages=0), h3.EINVAL), (dict(H=0), h3.EINVAL), (dict(d=96), 
              (dict(k=FAKE + 8), h3.EALIGN), (dict(k_scale=FAKE + 2), h3.EALIGN), (dict(times=FAKE + 4), h3.EALIGN)]
 BAD_BATCH = [(dict(B=0), h3.EINVAL), (dict(T=-1), h3.EINVAL), (dict(max_pages=0), h3.EINVAL),
              (dict(row_start=None), h3.EINVAL), (dict(page_table=None), h3.EINVAL), (dict(length=FAKE + 2), h3.EALIGN),
-             (dict(T=(1 << 30) + 1), h3.EUNSUPPORTED)]
+             (dict(T=(1 << 30) + 1), h3.EUNSUPPORTED), (dict(B=(1 << 16) + 1), h3.EUNSUPPORTED)]
 
 
 @pytest.mark.parametrize("call", [append, read, forward])

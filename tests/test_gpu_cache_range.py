@@ -1,12 +1,14 @@
 """The paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running maxima that rise
 again and again inside a step, V scales from nothing to 1e30, long caches of zeros, penalties that mask;
-workspaces that are not the device's; what the status word keeps; waits that run out."""
+workspaces that are not the device's; what the status word keeps; waits that run out;
+thousands of sequences."""
 import math
 
 import pytest
 import torch
 
 import biased_attention_video_b200 as h3
+from cache_ref import bounds
 from test_gpu_cache import DEV, check_forward, i32, make_cache, make_table
 
 pytestmark = pytest.mark.gpu
@@ -205,3 +207,42 @@ def test_tiles_give_up_and_recover(d, rows, length, pen):
         assert status == h3.ETIMEOUT or (polls > 1 and status == h3.OK and torch.equal(o, want)), polls
         o, _ = h3.cache_forward(c, *args, ws=ws, **more)
         assert h3.check(ws) == h3.OK and torch.equal(o, want), polls
+
+
+@pytest.mark.parametrize("B,H,max_rows", [(3000, 2, 2), (3000, 2, None), (65536, 1, 1), (65536, 1, None)])
+def test_thousands_of_sequences(B, H, max_rows):
+    """Sequences of at most four cached rows and one or two new ones, many of them empty: appended, read back, attended."""
+    d, g = 64, torch.Generator(device=DEV).manual_seed(B + H)
+    pick = lambda hi: torch.randint(0, hi, (B,), generator=g, device=DEV)
+    n = torch.minimum(pick(2 if max_rows == 1 else 3), pick(3))
+    length = pick(4)
+    n[-1], length[-1] = 1, 3
+    start = torch.cat([n.new_zeros(1), n.cumsum(0)]).to(torch.int32)
+    T = int(start[-1])
+    table = torch.randperm(B, generator=g, device=DEV).to(torch.int32)[:, None]
+    c = h3.Cache(*(torch.randint(-127, 128, (B, 1, 64, d), generator=g, device=DEV, dtype=torch.int8) for _ in range(2)),
+                 *(0.005 + 0.03 * torch.rand(B, 1, generator=g, device=DEV) for _ in range(2)))
+    ws = h3.cache_workspace(c, H, T, B)
+    held = length.to(torch.int32)
+    now = held + n.to(torch.int32)
+    x = torch.randn(2, 1, T, d, generator=g, device=DEV).to(torch.bfloat16)
+    h3.cache_append(c, x[0], x[1], start, held, table, ws=ws)
+    kb, vb = h3.cache_read(c, start, held, table, T=T, ws=ws)
+    seq = torch.repeat_interleave(torch.arange(B, device=DEV), n)
+    page = table[seq, 0].long()
+    for back, new, scale in ((kb, x[0], c.k_scale), (vb, x[1], c.v_scale)):
+        # half a step and its rounding in fp32, then the rounding to bf16
+        step = scale[page]
+        assert torch.all((back[0].float() - new[0].float()).abs() <= 0.501 * step + 2.0 ** -8 * (new[0].float().abs() + step))
+    q = torch.randn(H, T, d, generator=g, device=DEV).to(torch.bfloat16)
+    o, lse = h3.cache_forward(c, q, start, now, table, max_rows=max_rows, ws=ws, lse=True)
+    assert h3.check(ws) == h3.OK
+    k, v = ((codes[:, 0, :6].double() * scale.double()[..., None])[page] for codes, scale in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    s = torch.einsum("htd,tjd->htj", q.double(), k) / math.sqrt(d)
+    s = s.masked_fill(torch.arange(6, device=DEV) >= now[seq].long()[:, None], -math.inf)
+    ref_l = torch.logsumexp(s, -1)
+    w = torch.exp(s - ref_l[..., None])
+    reach = torch.einsum("htd,tjd->htj", q.double().abs(), k.abs()).amax(-1) / math.sqrt(d)
+    ref_o = torch.einsum("htj,tjd->htd", w, v)
+    tol_o, tol_l = bounds(ref_o, ref_l, torch.einsum("htj,tjd->htd", w, v.abs()), reach, 6, d)
+    assert torch.all((o.double() - ref_o).abs() <= tol_o) and torch.all((lse.double() - ref_l).abs() <= tol_l)
