@@ -1,7 +1,7 @@
 """The paged int8 cache at the ends of its range, against fp64 with the bounds of cache_ref: running maxima that rise
 again and again inside a step, V scales from nothing to 1e30, long caches of zeros, penalties that mask;
 workspaces that are not the device's; what the status word keeps; waits that run out;
-thousands of sequences."""
+thousands of sequences; calls behind one another and captured."""
 import math
 
 import pytest
@@ -246,3 +246,96 @@ def test_thousands_of_sequences(B, H, max_rows):
     ref_o = torch.einsum("htj,tjd->htd", w, v)
     tol_o, tol_l = bounds(ref_o, ref_l, torch.einsum("htj,tjd->htd", w, v.abs()), reach, 6, d)
     assert torch.all((o.double() - ref_o).abs() <= tol_o) and torch.all((lse.double() - ref_l).abs() <= tol_l)
+
+
+def test_captured_calls_behind_copies_and_joins():
+    """One graph: a copy, few rows, tiles on the same workspace, a merge, then few rows and tiles again behind work of
+    another stream; each replay with new queries and lengths equals the calls one by one."""
+    c, _ = make_cache(40, 2, 128, seed=9)
+    table = i32(make_table([1200, 1300], 40))
+    few, many = 3, 150
+    g = torch.Generator(device=DEV).manual_seed(0)
+    qs = torch.randn(4, 4, 2 * many, 128, generator=g, device=DEV).to(torch.bfloat16)
+    lens = [i32(x) for x in ([1200, 1300], [1, 700], [0, 65], [999, 128])]
+    start_few, start_many = i32([0, few, 2 * few]), i32([0, many, 2 * many])
+    side = torch.cuda.Stream()
+
+    def calls(q, x, length, ws):
+        here = torch.cuda.current_stream()
+        q.copy_(x)
+        a, la = h3.cache_forward(c, q[:, :2 * few], start_few, length, table, max_rows=few, ws=ws, lse=True)
+        b, lb = h3.cache_forward(c, q, start_many, length, table, max_rows=many, ws=ws, lse=True)
+        m, lm = h3.merge([b, b], [lb, lb], lse=True)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            twice = q * 2
+        here.wait_stream(side)
+        e, le = h3.cache_forward(c, twice[:, :2 * few], start_few, length, table, causal=True, max_rows=few, ws=ws, lse=True)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            thrice = twice * 1.5
+        here.wait_stream(side)
+        f, lf = h3.cache_forward(c, thrice, start_many, length, table, causal=True, max_rows=many, ws=ws, lse=True)
+        return a, la, b, lb, m, lm, e, le, f, lf
+
+    ws = [h3.cache_workspace(c, 4, 2 * many, 2) for _ in range(2)]
+    q = [qs[0].clone() for _ in range(2)]
+    x_in, len_in = qs[0].clone(), lens[0].clone()
+    calls(q[0], x_in, len_in, ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(q[0], x_in, len_in, ws[0])
+    for _ in range(3):
+        for x, length in zip(qs, lens):
+            x_in.copy_(x), len_in.copy_(length)
+            graph.replay()
+            want = calls(q[1], x, length, ws[1])
+            for i, (a, b) in enumerate(zip(got, want)):
+                assert torch.equal(a.nan_to_num(), b.nan_to_num()), i
+    assert h3.check(ws[0]) == h3.OK and h3.check(ws[1]) == h3.OK
+
+
+def test_calls_right_behind_one_another():
+    """Append, few rows and tiles in turn without a pause, one workspace, the length moving on the device: as with a
+    synchronisation after every call."""
+    out = []
+    for pause in (False, True):
+        c, _ = make_cache(30, 2, 64, seed=3)
+        table = i32(make_table([600, 900], 30))
+        g = torch.Generator(device=DEV).manual_seed(5)
+        ws = h3.cache_workspace(c, 6, 240, 2)
+        length, res = i32([3, 64]), []
+        for i, n in enumerate([1, 120, 2, 1, 64, 5, 120, 1, 1, 3]):
+            start = i32([0, n, 2 * n])
+            x = torch.randn(10, 2 * n, 64, generator=g, device=DEV).to(torch.bfloat16)
+            h3.cache_append(c, x[:2], x[2:4], start, length, table, ws=ws)
+            if pause:
+                torch.cuda.synchronize()
+            length += n
+            res += h3.cache_forward(c, x[4:], start, length, table, causal=True, max_rows=n, ws=ws, lse=True)
+            if pause:
+                torch.cuda.synchronize()
+        res += h3.cache_read(c, i32([0, 318, 636]), i32([3, 64]), table, T=636, ws=ws)
+        assert h3.check(ws) == h3.OK
+        out.append(res)
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("rows,bad", [(4, [1, 3]), (150, [0, 77])])
+def test_queries_that_are_not_finite_spoil_their_own_rows(rows, bad):
+    lengths = [64 * 5 + 7]
+    c, host = make_cache(6, 1, 128, seed=rows)
+    table = make_table(lengths, 6)
+    q = torch.randn(2, rows, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    args = i32([0, rows]), i32(lengths), i32(table)
+    want, want_l = h3.cache_forward(c, q, *args, lse=True)
+    q[:, bad[0], 5] = float("nan")
+    q[:, bad[1], 9] = float("inf")
+    o, lse = h3.cache_forward(c, q, *args, lse=True)
+    rest = [i for i in range(rows) if i not in bad]
+    assert torch.all(torch.isnan(o[:, bad])) and torch.all(torch.isnan(lse[:, bad]))
+    # the other rows' running maximum may lie elsewhere: twice the roundings of 2^-8 of probabilities and output
+    top = 127 * float(host[3].max())
+    assert torch.all((o[:, rest].float() - want[:, rest].float()).abs() <= 2.0 ** -6 * top)
+    assert torch.all((lse[:, rest] - want_l[:, rest]).abs() <= 2.0 ** -15)
