@@ -506,7 +506,9 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle 
 def cache_append(c: Cache, k, v, row_start, length, page_table, rope: Optional[Rope] = None, row_times=None, ws=None,
                  stream=None) -> None:
     """Append rows to the cache (h3attn_cache_append): k, v bf16 [H, T, d] (any head and row strides that are multiples
-    of 8), packed row row_start[b] + i becomes row length[b] + i of sequence b; keys rotated by ``rope``."""
+    of 8), packed row row_start[b] + i becomes row length[b] + i of sequence b; keys rotated by ``rope``.
+    Bad offsets, lengths, page ids and rotation indices are recorded in ``ws``, whose first 256 bytes the call uses:
+    check(ws) tells, and without a ws nothing does."""
     cs = c._c
     dev = c._t[0].get_device()
     T, kh, kr = _rows(k, "k", cs.H, cs.d, dev)
@@ -529,7 +531,9 @@ def cache_append(c: Cache, k, v, row_start, length, page_table, rope: Optional[R
 def cache_read(c: Cache, row_start, first, page_table, T: Optional[int] = None, k_out=None, v_out=None, ws=None,
                stream=None):
     """Cached rows as bf16 [H, T, d] (h3attn_cache_read): packed row row_start[b] + i gets row first[b] + i of sequence
-    b.  T packed rows, or the buffers k_out and v_out (both, or one for K or V alone); returns (k, v)."""
+    b.  T packed rows, or the buffers k_out and v_out (both, or one for K or V alone); returns (k, v).  Rows of new
+    buffers that belong to no sequence are not written.  Bad device values are recorded in ``ws`` as by
+    cache_append."""
     cs = c._c
     dev = c._t[0].get_device()
     with _on(dev, stream):
@@ -557,7 +561,9 @@ def cache_forward(c: Cache, q, row_start, length, page_table, causal: bool = Fal
     (h3attn_cache_forward); (o, lse) is one partition for merge().  The penalty needs q_times (float32 [T], NaN for
     rows without one) and the cache's times.  Rows of a new ``out`` that belong to no sequence are not written.  q . k /
     sqrt(d) and each row's largest score, penalty included, must stay below 2^23 in magnitude; beyond, the result is
-    undefined."""
+    undefined.  ``max_rows``, the most rows of a sequence in this call, is worth giving: without it the kernel is chosen
+    as if all T rows were one sequence's.  Bad device values and waits that gave up are recorded in ``ws`` (check(ws));
+    a call without one allocates and clears up to 39 MB and drops the record."""
     cs = c._c
     dev = c._t[0].get_device()
     T, qh, qr = _rows(q, "q", None, cs.d, dev)

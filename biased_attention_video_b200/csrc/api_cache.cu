@@ -53,8 +53,10 @@ int check_ws(const void* ws, size_t have, size_t need) {
 bool finite_nonneg(float x) { return std::isfinite(x) && x >= 0.0f; }
 
 // Up to this many (query row, head of the group) pairs of a sequence go through
-// the kernel for few rows.  Two sequences of 16,384 rows, 16 heads of 128: 32 pairs
-// take 68 us there and 84 us in tensor-core tiles, 33 to 64 pairs 118 and 78 us.
+// the kernel for few rows.  There / in tensor-core tiles, us, with 32 pairs, then 40:
+// 2 sequences of 16,384 rows, 16 heads of 128, 69 / 83, 97 / 82; one of 57,402, 8 heads,
+// 60 / 81, 85 / 81; 32 of 4,000, 8 heads, 125 / 152, 172 / 153; 8 of 2,000, 16 heads of
+// 64, 29 / 42, 38 / 43; one of 2,079, 56 heads of 128, 32 / 40, 36 / 41.
 constexpr long long kFewPairs = 32;
 
 // status word | the tile kernel's line [B + 1] | partial results.  A batch whose

@@ -5,14 +5,16 @@
 //   O = sum_j exp(s_j) code_j s_v / sum_j exp(s_j),   LSE = log sum_j exp(s_j);
 // a row that sees no key gets O = 0 and LSE = -inf.
 //
-// HBM-bound: a code is read once (twice for 17 to 32 pairs, then from L2) and used
-// for the few rows of one sequence and K/V head.  The query heads of a K/V head and
-// the rows of a sequence form one list of (row, head) pairs, cut into tiles of 8 NT
-// pairs; an item is one tile of one sequence and K/V head, its units are the
-// sequence's pages.  The units of all items form one line that the blocks share
-// evenly, whatever the lengths are (they are read on the device); a block walks its
-// stretch item by item, and items that lie in several blocks are joined by a second
-// launch from partial results (maximum, sum, unnormalised O in fp32).
+// A code is read once (twice for 17 to 32 pairs, then from L2) and used for the few
+// rows of one sequence and K/V head: HBM-bound up to 8 pairs, from 16 on by the
+// instructions per code (the same 134 MB with 8 / 16 / 32 pairs: 37 / 49 / 69 us).
+// The query heads of a K/V head and the rows of a sequence form one list of
+// (row, head) pairs, cut into tiles of 8 NT pairs; an item is one tile of one
+// sequence and K/V head, its units are the sequence's pages.  The units of all items
+// form one line that the blocks share evenly, whatever the lengths are (they are read
+// on the device); a block walks its stretch item by item, and items that lie in several
+// blocks are joined by a second launch from partial results (maximum, sum, unnormalised
+// O in fp32).
 //
 // Inside a block each warp streams granules of 32 keys on its own: cp.async into
 // a ring of its own (no barrier between warps until the item ends), then
@@ -32,11 +34,11 @@
 // a lane takes 16 consecutive bytes of a row per load.  mma.sync and not tcgen05:
 // 8 rows fill no 128-row tile, and the widened codes are in registers anyway.
 //
-// Measured: one row of 56 heads over 116,883 rows of 8 K/V heads of 128 (240 MB)
-// 52 us, 32 sequences of 410 to 8,192 rows (282 MB) 59 us: 4.6 and 4.8 TB/s, and
-// about 5.7 TB/s but for the 7 us that two launches and finding the pages take; the
-// same loop without its arithmetic takes 51.5 us and 60 us.  (A plain sum over 240 MB
-// reads 5.3 TB/s.)  In 16-key granules, 8 warps a block: 56 and 73 us.
+// Measured, from GPU to GPU: one row of 56 heads over 116,883 rows of 8 K/V heads of 128
+// (240 MB) 52 to 54 us, 32 sequences of 410 to 8,192 rows (282 MB) 59 to 64 us: 4.4 to
+// 4.8 TB/s, and 4.9 to 5.4 TB/s but for the 7 us that two launches and finding the pages
+// take; the same loop without its arithmetic takes 51.5 us and 60 us.  (A plain sum over
+// 240 MB reads 5.3 TB/s.)  In 16-key granules, 8 warps a block: 56 and 73 us.
 #include <cuda_bf16.h>
 
 #include <type_traits>

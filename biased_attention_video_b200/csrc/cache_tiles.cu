@@ -42,12 +42,12 @@
 // (maximum, sum, unnormalised O in fp32).  The line is laid out on the device
 // (plan_kernel), for the lengths are read there.
 //
-// Measured: 2,126 rows of 8 heads of 128 over 57,402 rows with the penalty 615 us
-// (810 TFLOP/s), causal chunks of four sequences of up to 2,500 rows, 16 heads on 4,
-// 349 us (700), 70 rows of 16 heads over 16,384 rows of two sequences 82 us.  What
-// bounds it is latency: a step takes about 4,400 cycles, its products 2,050; a
-// tile's scores, softmax (about 2,500 with both tiles at it) and products follow one
-// another, and the two tiles cover each other only in part.
+// Measured, from GPU to GPU: 2,126 rows of 8 heads of 128 over 57,402 rows with the penalty
+// 617 to 645 us (775 to 810 TFLOP/s), causal chunks of four sequences of up to 2,500
+// rows, 16 heads on 4, 334 to 352 us (695 to 735), 70 rows of 16 heads over 16,384 rows
+// of two sequences 82 us.  What bounds it is latency: a step takes about 4,400 cycles,
+// its products 2,050; a tile's scores, softmax (about 2,500 with both tiles at it) and
+// products follow one another, and the two tiles cover each other only in part.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -66,8 +66,9 @@ constexpr int kTile = 256;   // pairs of an item
 constexpr int kStep = 128;   // keys of a step
 constexpr int kGrid = 148;   // one block per SM
 // What beginning and ending an item costs (Q, the wait for the first step, the
-// output), in steps: it counts in the line (the causal chunks: 402 us without, 386
-// with 2, 375 with 4).
+// output), in steps: it counts in the line.  With 0 / 2 / 4 / 6 / 8 / 12 the causal
+// chunks take 374 / 350 / 343 / 337 / 331 / 337 us, 120 rows of 16 sequences of up to
+// 1,200 50 / 47 / 46 / 44 / 44 / 44 us, 70 rows over 16,384 86 / 84 / 82 / 82 / 85 / 86 us.
 constexpr int kItemCost = 6;
 constexpr long long kMinShare = kItemCost + 2;
 constexpr uint32_t kTmemCols = 512;
@@ -721,7 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const CacheAttnParam
         }
         umma_commit_one(s_full + 2 * sub + (x & 1u));
       };
-      auto wait_k = [&](int j) { return wait_bar_all<kSuspend>(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag); };
+      auto wait_k = [&](int j) {
+        return wait_bar_all<kSuspend>(k_full + ((done + j) & 1u), ((done + j) >> 1) & 1u, p, abort_flag);
+      };
       bool ok = wait_bar_all<kSuspend>(q_full, items & 1u, p, abort_flag) && wait_k(0);
       if (ok) {
         tc_fence_after();
