@@ -419,9 +419,12 @@ H3ATTN_API int h3attn_cache_read(const h3attn_cache* cache, const h3attn_batch* 
  * so that o and lse are one partition for h3attn_merge with any others.
  * q . k / sqrt(d) must stay below 2^23 in magnitude, and so must each row's
  * largest score, penalty included: larger ones are further apart in fp32 than a
- * softmax can tell, and the result is then undefined.  Below a row's largest
+ * softmax can tell, and the weights are then undefined.  Below a row's largest
  * score any finite penalty is right (it counts as 4.6e7 at most): a cap of 1e9
- * masks the keys beyond the window.
+ * masks the keys beyond the window.  A row all of whose keys are masked so has
+ * some mean of their values and an LSE near -4.6e7: nothing, in a merge.
+ * Cached values must stay below 2^96 in magnitude, for O is summed in fp32
+ * before it is normalised.
  * q: bf16 by strides, as k above; o: bf16 [H][T][d], 16-byte aligned; lse:
  * float32 [H][T] natural-log normaliser or NULL.  Rows that belong to no
  * sequence are left as they were.

@@ -92,6 +92,23 @@ def test_penalty_as_a_mask(cap, rows, one_time):
     check_forward(c, host, table, [n], [rows], 2, pen=(cap, 2.0, 0.01, cap), q_scale=60.0, seed=rows)
 
 
+@pytest.mark.parametrize("rows,one_time", [(2, True), (300, True), (300, False)])
+def test_rows_whose_keys_are_all_masked_count_nothing_in_a_merge(rows, one_time):
+    n = 64 * 6 + 9
+    c, host = make_cache(7, 2, 128, seed=rows, times=True)
+    c.times.fill_(5.0)
+    if not one_time:
+        c.times[:, ::2] = 7.0
+    q = 60 * torch.randn(2, rows, 128, device=DEV)
+    args = q.to(torch.bfloat16), i32([0, rows]), i32([n]), i32(make_table([n], 7))
+    o, lse = h3.cache_forward(c, *args, pen=(1e9, 2.0, 0.01, 1e9), q_times=torch.zeros(rows, device=DEV), lse=True)
+    top = 127 * float(host[3].max())
+    assert torch.all(o.abs() <= top * 1.02) and torch.all((lse + 2.0 ** 26 * math.log(2.0)).abs() <= 1e4)
+    p, lp = h3.cache_forward(c, *args, lse=True)
+    m, lm = h3.merge([o, p], [lse, lp], lse=True)
+    assert torch.equal(m, p) and torch.equal(lm, lp)
+
+
 V_SCALES = {  # pages of a sequence; what lies between is ordinary
     "pages of zero": {0: 0.0, 3: 0.0, 8: 0.0},
     "all zero": dict.fromkeys(range(9), 0.0),
