@@ -1,7 +1,6 @@
 """What the cache calls refuse, before any device work: through the C ABI with addresses that are never read, and
 through the Python binding with tensors of the wrong kind."""
 import ctypes
-import types
 
 import pytest
 import torch
@@ -42,7 +41,7 @@ BAD_CACHE = [(dict(n_pages=0), h3.EINVAL), (dict(H=0), h3.EINVAL), (dict(d=96), 
              (dict(k=FAKE + 8), h3.EALIGN), (dict(k_scale=FAKE + 2), h3.EALIGN), (dict(times=FAKE + 4), h3.EALIGN)]
 BAD_BATCH = [(dict(B=0), h3.EINVAL), (dict(T=-1), h3.EINVAL), (dict(max_pages=0), h3.EINVAL),
              (dict(row_start=None), h3.EINVAL), (dict(page_table=None), h3.EINVAL), (dict(length=FAKE + 2), h3.EALIGN),
-             (dict(T=(1 << 30) + 1), h3.EUNSUPPORTED), (dict(B=(1 << 16) + 1), h3.EUNSUPPORTED)]
+             (dict(T=(1 << 30) + 1), h3.EUNSUPPORTED)]
 
 
 @pytest.mark.parametrize("call", [append, read, forward])
@@ -111,19 +110,6 @@ def test_binding_refuses_wrong_tensors():
         h3.Rope(torch.zeros(4, 32), torch.zeros(4, 16))
     with pytest.raises(ValueError, match="index"):
         h3.Rope(torch.zeros(4, 32), torch.zeros(4, 32), index=torch.zeros(3))
-
-
-def test_binding_refuses_workspaces_and_streams_of_other_devices():
-    """The kernels would take a foreign address, or run on another device's stream."""
-    ws = torch.zeros(256, dtype=torch.uint8)
-    for dev in (0, 1):
-        with pytest.raises(ValueError, match=f"ws must be contiguous on cuda:{dev}, not on cpu"):
-            h3._space(ws, dev)
-    with pytest.raises(ValueError, match="ws must be contiguous"):
-        h3._space(ws[:1].expand(1 << 20), ws.get_device())
-    assert h3._space(ws, ws.get_device()) is ws
-    with pytest.raises(ValueError, match="stream must be one of cuda:0, not of cuda:1"):
-        h3._on(0, types.SimpleNamespace(device_index=1))
 
 
 def test_structs_match_the_header():
